@@ -271,11 +271,16 @@ def run(state):
 
 
 # ----------------------------------------------------------------------------- 64 bits
+def _pow2(e):
+    """2^e in double, exactly (a power function need not be), for integers e within the normal range."""
+    return ((e.long() + 1023) << 52).view(torch.float64)
+
+
 def _decode(codes):
     """E4M3 codes (uint8) -> doubles, from the format's definition."""
     c = torch.arange(256, device=codes.device)
     e, m = (c >> 3) & 15, (c & 7).double()
-    mag = torch.where(e == 0, m / 8 * 2.0 ** -6, (1 + m / 8) * torch.pow(2.0, (e - 7).double()))
+    mag = torch.where(e == 0, m / 8 * 2.0 ** -6, (1 + m / 8) * _pow2(e - 7))
     table = torch.where(c >= 128, -mag, mag)
     return table[codes.long()]
 
@@ -299,7 +304,7 @@ def _exact_quantized(x):
     for c in range(0, H, 128):
         v = x[:, c:c + 128].double()
         amax = v.abs().amax(1, keepdim=True).clamp(min=1e-10)
-        scale = torch.pow(2.0, torch.ceil(torch.log2(amax / 448)))
+        scale = _pow2(torch.ceil(torch.log2(amax / 448)))
         u = (v.abs() / scale).clamp(max=448.0)
         hi = torch.searchsorted(grid, u.contiguous()).clamp(1, 126)
         lo = hi - 1
