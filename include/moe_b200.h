@@ -73,6 +73,7 @@ extern "C" {
 #define MOE_DTYPE_FP8_E4M3 1 /* E4M3 codes + one fp32 scale per 128 x 128 block */
 #define MOE_DTYPE_MXFP8_E4M3 2 /* E4M3 codes + one E8M0 (power-of-two) scale per 32 elements of a row;
                                  normal tiles only (mode NORMAL, block_m 128) */
+#define MOE_DTYPE_FP32 3       /* output type of the stand-alone matrix products only */
 
 /*
  * MXFP8 scale-factor layout ("SF atoms"), used for MXFP8 weights and for the
@@ -431,6 +432,120 @@ MOE_API int moe_combine_reduce_scatter(int32_t T, int32_t topk, int32_t H, int32
 MOE_API int moe_combine_reduce_scatter_emulated(int32_t T, int32_t topk, int32_t H, int32_t world,
                                                 const moe_allreduce_rank* ranks, uint32_t epoch,
                                                 uint32_t timeout_us, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Stand-alone operators next to the layer: what a model runs in front of it,
+ * beside it and, in training, behind it.  They follow the conventions above
+ * (device pointers, asynchronous on `stream`, arguments checked first) and
+ * have no counterpart on the pages.  Rows may lie further apart than they are
+ * long: ld* is the distance of two rows in elements, at least the row's length
+ * and a multiple of 16 bytes; row pointers are 16-byte aligned.
+ *
+ * FP8 rows.  A [rows, cols] matrix of E4M3 codes (contiguous) with one fp32
+ * power-of-two scale per row and 128 columns, scales [ceil(cols / 128), rows]
+ * (K-block major, as a1_scale above): element (r, c) stands for
+ * code * scales[c / 128][r].  scale = the smallest power of two >=
+ * fp32(max(amax, 1e-10)) * fp32(1/448), code = e4m3(x / scale) (exact
+ * division, round to nearest even) -- the layer's own rule.  amax is taken
+ * over the finite values; infinities and NaN become the NaN code.
+ * cols is a multiple of 16; the last scale may cover fewer than 128 columns.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * RMS norm, with the residual's addition:
+ *   s = bf16(x + residual), or x without residual;
+ *   r = 1 / sqrt(mean(s^2) + eps);   y = bf16(s * r * weight)
+ * and, where codes is given, the FP8 rows of y (of the rounded y: the codes
+ * are those that quantising y afterwards would give).
+ *   x [T, H] bf16; residual and residual_out [T, H] bf16, both or neither:
+ *   residual_out receives s.  weight [H] bf16.
+ *   y [T, H] bf16, codes [T, H] with scales [ceil(H / 128), T], rstd [T] fp32
+ *   (receives r, for the backward pass): each may be NULL.
+ * H is a multiple of 8 up to 16384 (of 16 with codes).  residual_out may be
+ * residual or x, y may be any of the inputs [T, H] that residual_out is not.
+ * Sums are fp32: a row whose squares add up to more than fp32 holds gives 0.
+ */
+MOE_API int moe_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr, void* residual_out,
+                         int64_t ldo, const void* weight, float eps, int32_t T, int32_t H, void* y, int64_t ldy,
+                         uint8_t* codes, float* scales, float* rstd, void* stream);
+
+/* Workspace bytes of moe_rms_norm_backward (0 on invalid arguments and for T = 0). */
+MOE_API size_t moe_rms_norm_backward_workspace_size(int32_t T, int32_t H);
+
+/*
+ * Backward pass of the RMS norm.  With n = s * rstd, a = dy * weight:
+ *   dx = rstd * (a - n * mean(a * n)) + dresidual      (bf16)
+ *   dweight = sum over the rows of dy * n              (fp32, overwritten)
+ *   dy [T, H] bf16; s [T, H] bf16: the rows that were normalised (x, or
+ *   residual_out); rstd [T] from the forward pass; dresidual [T, H] bf16 or
+ *   NULL: the gradient that reaches s by other ways (dx is then the gradient
+ *   of x and of residual alike).  dx may be dy, s or dresidual.
+ *   ws: moe_rms_norm_backward_workspace_size() bytes, 16-byte aligned; two
+ *   calls that overlap on the device must not share it.
+ * Deterministic: the sums' order depends on T and H only.
+ */
+MOE_API int moe_rms_norm_backward(const void* dy, int64_t lddy, const void* s, int64_t lds, const void* weight,
+                                  const float* rstd, const void* dresidual, int64_t lddres, int32_t T, int32_t H,
+                                  void* dx, int64_t lddx, float* dweight, void* ws, size_t ws_bytes, void* stream);
+
+/* bf16 rows x [rows, cols] -> FP8 rows.  rows < 2^31, cols up to 2^20. */
+MOE_API int moe_quantize_rows_fp8(const void* x, int64_t ldx, int64_t rows, int32_t cols, uint8_t* codes,
+                                  float* scales, void* stream);
+
+/* FP8 rows -> bf16 rows x [rows, cols] (exact for scales that moe_quantize_rows_fp8 or moe_rms_norm wrote). */
+MOE_API int moe_dequantize_rows_fp8(const uint8_t* codes, const float* scales, int64_t rows, int32_t cols, void* x,
+                                    int64_t ldx, void* stream);
+
+/*
+ * Matrix products grouped by expert: group g owns rows offsets[g] ..
+ * offsets[g + 1] - 1 of x and y (rows sorted by expert, no padding needed;
+ * groups may be empty), and
+ *   forward   y [M, N]  : y[r] = x[r] . w[g(r)]^T
+ *   dx        dx [M, K] : dx[r] = dy[r] . w[g(r)]
+ *   dw        dw [G, N, K]: dw[g] = sum over g's rows of dy[r]^T x[r]; zero for an
+ *             empty group, or with accumulate = 1 added to what dw holds.
+ *   x [M, K] and dy [M, N] bf16, w [G, N, K] bf16 contiguous; the FP8 form takes
+ *   FP8 rows x and E4M3 weights w with w_scale [G, ceil(N / 128), ceil(K / 128)]
+ *   fp32 (moe_quantize_weights_fp8's layout).
+ *   offsets [G + 1] int32 on the device, ascending, within [0, M]; rows before
+ *   offsets[0] and from offsets[G] on belong to no group: they are not read
+ *   into any result and the rows of y and dx there are left as they were.
+ *   (Offsets are clamped to [0, M] and a group that ends before it starts is
+ *   empty, so bad offsets give undefined results but no bad access.)
+ *   NULL offsets with G = 1: one group of all rows.
+ *   out_dtype: MOE_DTYPE_BF16 or MOE_DTYPE_FP32 (accumulate needs FP32).
+ *   status: int32 device word that receives MOE_STATUS_WAIT_TIMEOUT | site if a
+ *   bounded in-kernel wait runs out (never cleared here), or NULL.
+ * 1 <= G <= 1024; N and K are multiples of 8 (FP8: K of 16).  Accumulation is
+ * fp32 and each result is rounded once; results do not depend on timing.
+ * The outputs must not overlap the inputs.
+ */
+MOE_API int moe_grouped_matmul(const void* x, int64_t ldx, const void* w, const int32_t* offsets, int32_t M,
+                               int32_t G, int32_t N, int32_t K, void* y, int64_t ldy, int32_t out_dtype,
+                               int32_t* status, void* stream);
+MOE_API int moe_grouped_matmul_fp8(const uint8_t* x, const float* x_scale, const uint8_t* w, const float* w_scale,
+                                   const int32_t* offsets, int32_t M, int32_t G, int32_t N, int32_t K, void* y,
+                                   int64_t ldy, int32_t out_dtype, int32_t* status, void* stream);
+MOE_API int moe_grouped_matmul_dx(const void* dy, int64_t lddy, const void* w, const int32_t* offsets, int32_t M,
+                                  int32_t G, int32_t N, int32_t K, void* dx, int64_t lddx, int32_t out_dtype,
+                                  int32_t* status, void* stream);
+MOE_API int moe_grouped_matmul_dw(const void* dy, int64_t lddy, const void* x, int64_t ldx, const int32_t* offsets,
+                                  int32_t M, int32_t G, int32_t N, int32_t K, void* dw, int32_t out_dtype,
+                                  int32_t accumulate, int32_t* status, void* stream);
+
+/*
+ * FP8 matrix product with block scales, y [M, N] = x . w^T: FP8 rows x [M, K]
+ * and one weight w [N, K] E4M3 with w_scale [ceil(N / 128), ceil(K / 128)]
+ * (moe_quantize_weights_fp8; a weight whose sizes are no multiples of 128 is
+ * padded with zeros, quantised, and cut).  The products of each 128-deep block
+ * are summed and multiplied by the two scales, the blocks are summed in fp32.
+ * Types, status and limits are those of the grouped products.
+ */
+MOE_API int moe_matmul_fp8(const uint8_t* x, const float* x_scale, const uint8_t* w, const float* w_scale, int32_t M,
+                           int32_t N, int32_t K, void* y, int64_t ldy, int32_t out_dtype, int32_t* status,
+                           void* stream);
 
 /* Library version: major * 10000 + minor * 100 + patch. */
 MOE_API int32_t moe_version(void);

@@ -8,6 +8,7 @@
 #include <string>
 
 #include "allreduce.h"
+#include "api_internal.h"
 #include "kernels.h"
 #include "moe_b200.h"
 
@@ -56,6 +57,23 @@ int device_check(int* sms) {
   if (sms) *sms = cache_sms[dev];
   return MOE_OK;
 }
+
+}  // namespace
+
+// shared with the other translation units of the C ABI
+int moe::api_fail(int code, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  g_last_error = buf;
+  return code;
+}
+
+int moe::api_device_check(int* sms) { return device_check(sms); }
+
+namespace {
 
 inline int64_t align256(int64_t v) { return (v + 255) & ~int64_t(255); }
 

@@ -31,6 +31,7 @@ MOE_STATUS_WAIT_TIMEOUT = 0x100
 DTYPE_BF16 = 0
 DTYPE_FP8_E4M3 = 1
 DTYPE_MXFP8_E4M3 = 2
+DTYPE_FP32 = 3
 
 MODE_AUTO = 0
 MODE_NORMAL = 1
@@ -46,7 +47,10 @@ EXPORTED = (
     "moe_fused_forward", "moe_forward_stages", "moe_read_status", "moe_version", "moe_align_noalloc",
     "moe_selftest_wait_timeout", "moe_quantize_weights_mxfp8", "moe_combine_allreduce_flag_count",
     "moe_combine_allreduce", "moe_combine_allreduce_emulated", "moe_combine_reduce_scatter_flag_count",
-    "moe_combine_reduce_scatter", "moe_combine_reduce_scatter_emulated",
+    "moe_combine_reduce_scatter", "moe_combine_reduce_scatter_emulated", "moe_rms_norm",
+    "moe_rms_norm_backward_workspace_size", "moe_rms_norm_backward", "moe_quantize_rows_fp8",
+    "moe_dequantize_rows_fp8", "moe_grouped_matmul", "moe_grouped_matmul_fp8", "moe_grouped_matmul_dx",
+    "moe_grouped_matmul_dw", "moe_matmul_fp8",
 )
 
 MAX_RANKS = 16
@@ -127,6 +131,19 @@ def lib():
             "moe_combine_reduce_scatter_emulated": (ctypes.c_int, [i32, i32, i32, i32,
                                                                    ctypes.POINTER(MoeAllreduceRank),
                                                                    ctypes.c_uint32, ctypes.c_uint32, vp]),
+            "moe_rms_norm": (ctypes.c_int, [vp, i64, vp, i64, vp, i64, vp, ctypes.c_float, i32, i32, vp, i64, vp, vp,
+                                            vp, vp]),
+            "moe_rms_norm_backward_workspace_size": (sz, [i32, i32]),
+            "moe_rms_norm_backward": (ctypes.c_int, [vp, i64, vp, i64, vp, vp, vp, i64, i32, i32, vp, i64, vp, vp,
+                                                     sz, vp]),
+            "moe_quantize_rows_fp8": (ctypes.c_int, [vp, i64, i64, i32, vp, vp, vp]),
+            "moe_dequantize_rows_fp8": (ctypes.c_int, [vp, vp, i64, i32, vp, i64, vp]),
+            "moe_grouped_matmul": (ctypes.c_int, [vp, i64, vp, vp, i32, i32, i32, i32, vp, i64, i32, vp, vp]),
+            "moe_grouped_matmul_fp8": (ctypes.c_int, [vp, vp, vp, vp, vp, i32, i32, i32, i32, vp, i64, i32, vp, vp]),
+            "moe_grouped_matmul_dx": (ctypes.c_int, [vp, i64, vp, vp, i32, i32, i32, i32, vp, i64, i32, vp, vp]),
+            "moe_grouped_matmul_dw": (ctypes.c_int, [vp, i64, vp, i64, vp, i32, i32, i32, i32, vp, i32, i32, vp,
+                                                     vp]),
+            "moe_matmul_fp8": (ctypes.c_int, [vp, vp, vp, vp, i32, i32, i32, vp, i64, i32, vp, vp]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -392,3 +409,244 @@ def combine_reduce_scatter_emulated(T, topk, H, ranks, epoch, timeout_us=2_000_0
     _check(lib().moe_combine_reduce_scatter_emulated(int(T), int(topk), int(H), len(ranks), arr, int(epoch),
                                                      int(timeout_us), _stream(stream)))
 
+
+
+# ----------------------------------------------------------------------------- stand-alone operators
+# Tensors of other types, shapes, devices or layouts than a function documents raise ValueError here; what
+# the C ABI checks (sizes, alignment) raises MoeError.  The work runs on `stream`, or on the current stream
+# of the tensors' device.
+_OUT_DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_FP32}
+
+
+def _require(name: str, t, dtype, shape, device, *, rows=False):
+    """``t`` is a CUDA tensor of this type, shape and device: contiguous, or (``rows``) with unit stride along
+    its last dimension."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name}: a tensor is needed, got {type(t).__name__}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: type {t.dtype}, {dtype} is needed")
+    if t.device != device or device.type != "cuda":
+        raise ValueError(f"{name}: on {t.device}, needed on the CUDA device of the first argument ({device})")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, {tuple(shape)} is needed")
+    if not t.is_contiguous() and not (rows and t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] == 1)):
+        raise ValueError(f"{name}: " + ("its last dimension must have stride 1" if rows else "must be contiguous"))
+    return t
+
+
+def _2d(name: str, t):
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name}: a 2-dimensional tensor is needed")
+    return t.shape
+
+
+def _ld(t) -> int:
+    """Elements between the rows of a 2-D tensor (a single row's stride says nothing)."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+def _run(fn, device, stream, *args):
+    """Call a C entry point on the tensors' device, whichever device is current."""
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _run(fn, device, stream, *args)
+    s = torch.cuda.current_stream(device) if stream is None else stream
+    _check(fn(*args, ctypes.c_void_p(s.cuda_stream)))
+
+
+def _out(name, out, shape, dtype, device):
+    """``out`` checked, or a new tensor."""
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    return _require(name, out, dtype, shape, device, rows=True)
+
+
+def _out_dtype(out, out_dtype):
+    dtype = out_dtype if out is None or out_dtype is not None else out.dtype
+    dtype = torch.bfloat16 if dtype is None else dtype
+    if dtype not in _OUT_DTYPES:
+        raise ValueError(f"out_dtype: {dtype}, torch.bfloat16 or torch.float32 is needed")
+    return dtype
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, *, residual=None, residual_out=None, y=True,
+             fp8=False, rstd=False, stream=None) -> dict:
+    """RMS norm of the rows of x [T, H] bf16, after the addition of ``residual`` if given.
+
+    Returns a dict: ``residual`` (bf16(x + residual), written to ``residual_out`` if given, which may be the
+    residual itself; None without residual), ``y`` (bf16 [T, H]; True allocates it, a tensor receives it, False
+    leaves it out), ``codes`` and ``scales`` (with ``fp8``: the FP8 rows of y, uint8 [T, H] and fp32
+    [ceil(H / 128), T]) and ``rstd`` (fp32 [T] if asked for)."""
+    T, H = _2d("x", x)
+    dev = x.device
+    _require("x", x, torch.bfloat16, (T, H), dev, rows=True)
+    _require("weight", weight, torch.bfloat16, (H,), dev)
+    if residual is not None:
+        _require("residual", residual, torch.bfloat16, (T, H), dev, rows=True)
+        residual_out = _out("residual_out", residual_out, (T, H), torch.bfloat16, dev)
+    elif residual_out is not None:
+        raise ValueError("residual_out: given without residual")
+    if y is True or y is False or y is None:
+        y = torch.empty((T, H), dtype=torch.bfloat16, device=dev) if y else None
+    else:
+        _require("y", y, torch.bfloat16, (T, H), dev, rows=True)
+    codes = torch.empty((T, H), dtype=torch.uint8, device=dev) if fp8 else None
+    scales = torch.empty(((H + 127) // 128, T), dtype=torch.float32, device=dev) if fp8 else None
+    r = torch.empty((T,), dtype=torch.float32, device=dev) if rstd else None
+    _run(lib().moe_rms_norm, dev, stream, _ptr(x), _ld(x), _ptr(residual), 0 if residual is None else _ld(residual),
+         _ptr(residual_out), 0 if residual is None else _ld(residual_out), _ptr(weight), eps, T, H, _ptr(y),
+         0 if y is None else _ld(y), _ptr(codes), _ptr(scales), _ptr(r))
+    return {"residual": residual_out, "y": y, "codes": codes, "scales": scales, "rstd": r}
+
+
+def rms_norm_backward(dy: torch.Tensor, s: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor, *, dresidual=None,
+                      dx=None, ws=None, stream=None):
+    """Backward pass of :func:`rms_norm`: (dx bf16 [T, H], dweight fp32 [H]).
+
+    ``s`` is what was normalised (x, or the ``residual`` that the forward pass returned), ``dresidual`` the
+    gradient that reaches it by other ways; ``ws`` a uint8 workspace of
+    ``moe_rms_norm_backward_workspace_size`` bytes (allocated if not given)."""
+    T, H = _2d("dy", dy)
+    dev = dy.device
+    _require("dy", dy, torch.bfloat16, (T, H), dev, rows=True)
+    _require("s", s, torch.bfloat16, (T, H), dev, rows=True)
+    _require("weight", weight, torch.bfloat16, (H,), dev)
+    _require("rstd", rstd, torch.float32, (T,), dev)
+    if dresidual is not None:
+        _require("dresidual", dresidual, torch.bfloat16, (T, H), dev, rows=True)
+    dx = _out("dx", dx, (T, H), torch.bfloat16, dev)
+    dweight = torch.empty((H,), dtype=torch.float32, device=dev)
+    if ws is None:
+        ws = torch.empty((max(int(lib().moe_rms_norm_backward_workspace_size(T, H)), 16),), dtype=torch.uint8,
+                         device=dev)
+    else:
+        _require("ws", ws, torch.uint8, ws.shape, dev)
+    _run(lib().moe_rms_norm_backward, dev, stream, _ptr(dy), _ld(dy), _ptr(s), _ld(s), _ptr(weight), _ptr(rstd),
+         _ptr(dresidual), 0 if dresidual is None else _ld(dresidual), T, H, _ptr(dx), _ld(dx), _ptr(dweight), _ptr(ws),
+         ws.numel())
+    return dx, dweight
+
+
+def quantize_rows_fp8(x: torch.Tensor, stream=None):
+    """bf16 [rows, cols] -> FP8 rows: (E4M3 codes as uint8 [rows, cols], fp32 scales [ceil(cols / 128), rows])."""
+    rows, cols = _2d("x", x)
+    _require("x", x, torch.bfloat16, (rows, cols), x.device, rows=True)
+    codes = torch.empty((rows, cols), dtype=torch.uint8, device=x.device)
+    scales = torch.empty(((cols + 127) // 128, rows), dtype=torch.float32, device=x.device)
+    _run(lib().moe_quantize_rows_fp8, x.device, stream, _ptr(x), _ld(x), rows, cols, _ptr(codes), _ptr(scales))
+    return codes, scales
+
+
+def dequantize_rows_fp8(codes: torch.Tensor, scales: torch.Tensor, *, out=None, stream=None):
+    """FP8 rows -> the bf16 [rows, cols] values that they stand for."""
+    rows, cols = _2d("codes", codes)
+    dev = codes.device
+    _require("codes", codes, torch.uint8, (rows, cols), dev)
+    _require("scales", scales, torch.float32, ((cols + 127) // 128, rows), dev)
+    out = _out("out", out, (rows, cols), torch.bfloat16, dev)
+    _run(lib().moe_dequantize_rows_fp8, dev, stream, _ptr(codes), _ptr(scales), rows, cols, _ptr(out), _ld(out))
+    return out
+
+
+def _weight(name, w, dtype, dev):
+    if not isinstance(w, torch.Tensor) or w.dim() != 3:
+        raise ValueError(f"{name}: a 3-dimensional tensor [groups, N, K] is needed")
+    return _require(name, w, dtype, w.shape, dev).shape
+
+
+def _offsets(offsets, G, dev):
+    if offsets is None:
+        if G != 1:
+            raise ValueError(f"offsets: needed for {G} groups")
+        return None
+    return _require("offsets", offsets, torch.int32, (G + 1,), dev)
+
+
+def matmul_fp8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, *, out=None,
+               out_dtype=None, status=None, stream=None):
+    """y [M, N] = x . w^T of FP8 rows x [M, K] (codes and scales of :func:`quantize_rows_fp8` or
+    :func:`rms_norm`) and a weight w [N, K] with one scale per 128 x 128 block; bf16 or fp32."""
+    M, K = _2d("x", x)
+    N = _2d("w", w)[0]
+    dev = x.device
+    _require("x", x, torch.uint8, (M, K), dev)
+    _require("x_scale", x_scale, torch.float32, ((K + 127) // 128, M), dev)
+    _require("w", w, torch.uint8, (N, K), dev)
+    _require("w_scale", w_scale, torch.float32, ((N + 127) // 128, (K + 127) // 128), dev)
+    dtype = _out_dtype(out, out_dtype)
+    out = _out("out", out, (M, N), dtype, dev)
+    _run(lib().moe_matmul_fp8, dev, stream, _ptr(x), _ptr(x_scale), _ptr(w), _ptr(w_scale), M, N, K, _ptr(out),
+         _ld(out), _OUT_DTYPES[dtype], _status_ptr(status, dev))
+    return out
+
+
+def _status_ptr(status, dev):
+    return None if status is None else _ptr(_require("status", status, torch.int32, (1,), dev))
+
+
+def grouped_matmul(x: torch.Tensor, w: torch.Tensor, offsets, *, x_scale=None, w_scale=None, out=None, out_dtype=None,
+                   status=None, stream=None):
+    """y[r] = x[r] . w[g]^T for the rows offsets[g] <= r < offsets[g + 1] of every group g.
+
+    x [M, K] bf16 and w [G, N, K] bf16; or FP8 rows x with ``x_scale`` [ceil(K / 128), M] and E4M3 weights with
+    ``w_scale`` [G, ceil(N / 128), ceil(K / 128)].  ``offsets`` int32 [G + 1] on the device (None: one group of
+    all rows).  y [M, N] bf16 or fp32; rows of no group are not written."""
+    M, K = _2d("x", x)
+    dev = x.device
+    if (x_scale is None) != (w_scale is None):
+        raise ValueError("x_scale and w_scale: give both (FP8) or neither (bf16)")
+    fp8 = x_scale is not None
+    G, N, _ = _weight("w", w, torch.uint8 if fp8 else torch.bfloat16, dev)
+    _require("w", w, w.dtype, (G, N, K), dev)
+    _require("x", x, torch.uint8 if fp8 else torch.bfloat16, (M, K), dev, rows=not fp8)
+    _offsets(offsets, G, dev)
+    dtype = _out_dtype(out, out_dtype)
+    out = _out("out", out, (M, N), dtype, dev)
+    if fp8:
+        _require("x_scale", x_scale, torch.float32, ((K + 127) // 128, M), dev)
+        _require("w_scale", w_scale, torch.float32, (G, (N + 127) // 128, (K + 127) // 128), dev)
+        _run(lib().moe_grouped_matmul_fp8, dev, stream, _ptr(x), _ptr(x_scale), _ptr(w), _ptr(w_scale), _ptr(offsets),
+             M, G, N, K, _ptr(out), _ld(out), _OUT_DTYPES[dtype], _status_ptr(status, dev))
+    else:
+        _run(lib().moe_grouped_matmul, dev, stream, _ptr(x), _ld(x), _ptr(w), _ptr(offsets), M, G, N, K, _ptr(out),
+             _ld(out), _OUT_DTYPES[dtype], _status_ptr(status, dev))
+    return out
+
+
+def grouped_matmul_dx(dy: torch.Tensor, w: torch.Tensor, offsets, *, out=None, out_dtype=None, status=None,
+                      stream=None):
+    """Gradient of :func:`grouped_matmul`'s rows: dx[r] = dy[r] . w[g] (dy [M, N], w [G, N, K] bf16 -> [M, K])."""
+    M, N = _2d("dy", dy)
+    dev = dy.device
+    G, _, K = _weight("w", w, torch.bfloat16, dev)
+    _require("w", w, torch.bfloat16, (G, N, K), dev)
+    _require("dy", dy, torch.bfloat16, (M, N), dev, rows=True)
+    _offsets(offsets, G, dev)
+    dtype = _out_dtype(out, out_dtype)
+    out = _out("out", out, (M, K), dtype, dev)
+    _run(lib().moe_grouped_matmul_dx, dev, stream, _ptr(dy), _ld(dy), _ptr(w), _ptr(offsets), M, G, N, K, _ptr(out),
+         _ld(out), _OUT_DTYPES[dtype], _status_ptr(status, dev))
+    return out
+
+
+def grouped_matmul_dw(dy: torch.Tensor, x: torch.Tensor, offsets, *, out=None, out_dtype=None, accumulate=False,
+                      status=None, stream=None):
+    """Gradient of :func:`grouped_matmul`'s weights: dw[g] = sum of dy[r]^T x[r] over the group's rows (dy [M, N],
+    x [M, K] bf16 -> [G, N, K] bf16 or fp32; zero for an empty group).  ``accumulate`` adds to an fp32 ``out``."""
+    M, N = _2d("dy", dy)
+    K = _2d("x", x)[1]
+    dev = dy.device
+    _require("dy", dy, torch.bfloat16, (M, N), dev, rows=True)
+    _require("x", x, torch.bfloat16, (M, K), dev, rows=True)
+    G = 1 if offsets is None else offsets.numel() - 1
+    _offsets(offsets, G, dev)
+    if accumulate and out is None:
+        raise ValueError("accumulate: needs out")
+    dtype = _out_dtype(out, out_dtype)
+    if out is None:
+        out = torch.empty((G, N, K), dtype=dtype, device=dev)
+    else:
+        _require("out", out, dtype, (G, N, K), dev)
+    _run(lib().moe_grouped_matmul_dw, dev, stream, _ptr(dy), _ld(dy), _ptr(x), _ld(x), _ptr(offsets), M, G, N, K,
+         _ptr(out), _OUT_DTYPES[dtype], 1 if accumulate else 0, _status_ptr(status, dev))
+    return out
