@@ -33,5 +33,6 @@ struct GroupedProblem {
 };
 
 cudaError_t launch_grouped(const GroupedProblem& p, cudaStream_t stream);
+cudaError_t launch_grouped_fp8(const GroupedProblem& p, cudaStream_t stream);
 
 }  // namespace moe

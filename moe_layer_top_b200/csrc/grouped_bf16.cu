@@ -1,0 +1,511 @@
+// bf16 matrix products grouped by expert with ragged sizes, on the
+// 5th-generation tensor cores (tcgen05, sm_100a).  Group g owns rows
+// [off[g], off[g + 1]):
+//
+//   forward : y[r, :]  = x[r, :] . w[g]^T
+//   dx      : dx[r, :] = dy[r, :] . w[g]
+//   dw      : dw[g]    = dy_g^T . x_g               (reduction over g's rows)
+//
+// No operand is copied, padded or transposed in memory: the tensor core reads
+// K-major tiles (x, dy, and w in the forward product) and MN-major tiles (w in
+// dx; dy and x in dw) alike, so every product takes the tensors as they lie.
+//
+// forward, dx: the weight fills the MMA's M side and the group's rows its N
+// side, because N comes in steps of 16 or 32 and M only whole: a group's rows
+// are cut into equal tiles of at most kRowTile, each rounded up by less than a
+// step, so a ragged group wastes little and one row costs little more than
+// its weights.  A tile that runs past its group's end computes rows of the
+// next group and does not store them.
+// dw: the rows are the reduction axis; those past the group's end in its last
+// stage are cleared in shared memory before the MMA reads them.
+//
+// kPair: a cluster of two CTAs computes a 256 x 256 tile (cta_group::2): each
+// SM loads 128 of the 256 A rows and half of the B rows, so a stage moves 32 KB
+// into an SM for 512 cycles of MMA, which the shared-memory port keeps up with
+// (a 128 x 256 tile of one SM needs 48 KB).  Without kPair one CTA computes
+// 128 x 128: more and smaller tiles for small problems.
+//
+// Persistent, 10 warps per CTA: TMA producer, MMA issuer (of the leader CTA),
+// eight epilogue warps; the accumulator is double-buffered in TMEM, so a
+// tile's stores run under the next tile's products.
+#include "grouped_common.cuh"
+
+namespace moe {
+
+namespace {
+
+struct Args {
+  int M, G;
+  int m_rows;        // rows of the MMA's M side: N (fwd, dw), K (dx)
+  int m_tiles;
+  int cols;          // dw: K
+  int n_tiles;       // dw: column tiles
+  int red;           // fwd: K, dx: N
+  const int32_t* offsets;
+  void* out;
+  long long ldo;     // fwd, dx: elements between rows of out
+  int out_f32, accumulate;
+  int* status;
+};
+
+template <int Kind, bool kPair>
+struct Cfg {
+  static constexpr int kCtas = kPair ? 2 : 1;
+  static constexpr int kMTile = 128 * kCtas;
+  static constexpr int kNTile = 128 * kCtas;           // most N columns of a tile
+  static constexpr int kABytes = 16384;                // 128 rows x 128 bytes
+  static constexpr int kBBytes = 16384;
+  static constexpr int kStageBytes = kABytes + kBBytes;
+  static constexpr bool kMnA = Kind != kGroupedFwd;
+  static constexpr bool kMnB = Kind == kGroupedDw;
+  static constexpr int kTmemCols = 2 * kNTile;
+  // dw: each epilogue thread stages 128 bytes of its row for one bulk copy (+ 16: rows spread over the banks)
+  static constexpr int kOutPitch = 144;
+  static constexpr int kOutBytes = Kind == kGroupedDw ? 256 * kOutPitch : 0;
+  static constexpr int kStages = (kSmemMax - 1024 - kGroupedReserve - kOutBytes) / kStageBytes;
+  static constexpr size_t kSmemBytes =
+      static_cast<size_t>(kStages) * kStageBytes + kOutBytes + kGroupedReserve + 1024;
+  static constexpr uint32_t kIdesc =
+      make_idesc(kMTile, 0, false) | (kMnA ? 1u << 15 : 0u) | (kMnB ? 1u << 16 : 0u);
+  static_assert(kStages >= 4 && kStages <= 16, "ring depth");
+};
+
+struct Tile {
+  int g;
+  int m0;         // first row of the M side
+  int n0, n;      // first N column (fwd, dx: row of the batch; dw: column of out) and the MMA's N
+  int valid;      // N columns to store
+  int red0, red;  // dw: the group's first row and row count; otherwise 0 and the reduction length
+};
+
+template <int Kind, bool kPair>
+__device__ __forceinline__ Tile tile_at(const Args& a, const int* off, const int* first, int t) {
+  using C = Cfg<Kind, kPair>;
+  Tile r;
+  if constexpr (Kind == kGroupedDw) {
+    const int per_group = a.m_tiles * a.n_tiles;
+    r.g = t / per_group;
+    const int i = t - r.g * per_group;
+    const int m = i / a.n_tiles;
+    r.m0 = m * C::kMTile;
+    r.n0 = (i - m * a.n_tiles) * C::kNTile;
+    r.n = C::kNTile;
+    r.valid = min(C::kNTile, a.cols - r.n0);
+    r.red0 = off[r.g];
+    r.red = max(0, off[r.g + 1] - r.red0);
+  } else {
+    r.g = group_of_tile(first, a.G, t);
+    const int i = t - first[r.g];
+    const int row0 = off[r.g], rows = off[r.g + 1] - row0;
+    const int parts = (rows + C::kNTile - 1) / C::kNTile;
+    constexpr int kStep = 16 * C::kCtas;  // granularity of N: each CTA of a pair loads half in boxes of 16
+    const int each = ((rows + parts - 1) / parts + kStep - 1) / kStep * kStep;  // <= kNTile
+    const int p = i / a.m_tiles;
+    r.m0 = (i - p * a.m_tiles) * C::kMTile;
+    r.n0 = row0 + p * each;
+    r.n = each;
+    r.valid = min(each, rows - p * each);  // at least one: rows > (parts - 1) * kNTile >= (parts - 1) * each
+    r.red0 = 0;
+    r.red = a.red;
+  }
+  return r;
+}
+
+template <int Kind, bool kPair>
+__global__ void __launch_bounds__(kGroupedThreads, 1)
+    grouped_bf16_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                        const __grid_constant__ CUtensorMap tm_b16, const Args args) {
+  using C = Cfg<Kind, kPair>;
+  // dw in a pair: each CTA counts its own copies, clears its own tail and tells the leader
+  constexpr bool kRelay = kPair && Kind == kGroupedDw;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* staging = smem + static_cast<size_t>(C::kStages) * C::kStageBytes;
+  uint8_t* reserve = staging + C::kOutBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(reserve);
+  uint64_t* empty = full + C::kStages;
+  uint64_t* peer_full = empty + C::kStages;
+  uint64_t* acc_full = peer_full + C::kStages;
+  uint64_t* acc_empty = acc_full + 2;
+  uint64_t* drain = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* scan = reinterpret_cast<int*>(reserve + 640);
+  int* off = reinterpret_cast<int*>(reserve + 1024);
+  int* first = off + kMaxGroups + 4;
+  static_assert((3 * C::kStages + 5) * 8 + 8 <= 640, "barriers overlap the scan buffer");
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = kPair ? static_cast<int>(cluster_rank()) : 0;
+  const bool leader = rank == 0;
+  pdl_launch_dependents();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+      mbar_init(&peer_full[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], kGroupedEpiWarps * C::kCtas);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_a);
+    tma_prefetch_desc(&tm_b);
+  }
+  if (warp == 1) tmem_alloc_for<kPair>(tmem_slot, C::kTmemCols);
+  pdl_wait();
+  tc_fence_before();
+  int num_tiles = build_group_tables(args.offsets, args.M, args.G, C::kNTile, args.m_tiles, off,
+                                     Kind == kGroupedDw ? nullptr : first, scan);
+  if constexpr (Kind == kGroupedDw) num_tiles = args.G * args.m_tiles * args.n_tiles;
+  if constexpr (kPair) cluster_barrier();  // the peer's barriers are initialised before any remote arrival
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const int first_tile = static_cast<int>(blockIdx.x) / C::kCtas, stride = static_cast<int>(gridDim.x) / C::kCtas;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ producer (of each CTA)
+    if (lane == 0) {
+      const uint64_t pol = policy_evict_normal();
+      int stage = 0;
+      uint32_t phase = 0;
+      long long fills = 0;
+      bool ok = true;
+      for (int t = first_tile; t < num_tiles && ok; t += stride) {
+        const Tile tl = tile_at<Kind, kPair>(args, off, first, t);
+        const int m0 = tl.m0 + 128 * rank;
+        const int half = tl.n / C::kCtas;           // N columns that this CTA loads
+        const int n0 = tl.n0 + half * rank;
+        const uint32_t bytes = C::kABytes + half * 128;
+        for (int k = 0; k < tl.red; k += 64) {
+          if (!wait_bar(&empty[stage], phase ^ 1u, abort_flag, args.status, kWhereGroupedProducer)) {
+            ok = false;
+            break;
+          }
+          uint8_t* a = smem + static_cast<size_t>(stage) * C::kStageBytes;
+          uint8_t* b = a + C::kABytes;
+          constexpr bool kLead = kPair && !kRelay;  // copies of both CTAs count on the leader's barrier
+          uint32_t bar = smem_u32(&full[stage]);
+          if constexpr (kLead) {
+            if (leader) mbar_arrive_expect_tx(&full[stage], 2 * bytes);
+            bar = in_cta(&full[stage], 0);
+          } else {
+            mbar_arrive_expect_tx(&full[stage], bytes);
+          }
+          if constexpr (Kind == kGroupedFwd) {
+            load_3d<kLead>(a, &tm_a, bar, k, m0, tl.g, pol);
+          } else if constexpr (Kind == kGroupedDx) {
+            load_3d<kLead>(a, &tm_a, bar, m0, k, tl.g, pol);
+            load_3d<kLead>(a + 8192, &tm_a, bar, m0 + 64, k, tl.g, pol);
+          } else {
+            load_2d<kLead>(a, &tm_a, bar, m0, tl.red0 + k, pol);
+            load_2d<kLead>(a + 8192, &tm_a, bar, m0 + 64, tl.red0 + k, pol);
+          }
+          if constexpr (Kind == kGroupedDw) {
+            load_2d<kLead>(b, &tm_b, bar, n0, tl.red0 + k, pol);
+            load_2d<kLead>(b + 8192, &tm_b, bar, n0 + 64, tl.red0 + k, pol);
+          } else {
+            int r = 0;
+            for (; r + 64 <= half; r += 64) load_2d<kLead>(b + r * 128, &tm_b, bar, k, n0 + r, pol);
+            for (; r < half; r += 16) load_2d<kLead>(b + r * 128, &tm_b16, bar, k, n0 + r, pol);
+          }
+          ++fills;
+          if (++stage == C::kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // (the leader's barriers count both CTAs' copies)
+      if (!ok && (kRelay || leader)) drain_copies(full, C::kStages, fills);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA issuer: the whole warp walks, lane 0 issues
+    int stage = 0, abuf = 0;
+    uint32_t phase = 0, aphase = 0;
+    bool ok = true;
+    if (leader || kRelay) {
+      for (int t = first_tile; t < num_tiles && ok; t += stride) {
+        const Tile tl = tile_at<Kind, kPair>(args, off, first, t);
+        if (tl.red == 0) continue;
+        if (leader) {
+          ok = warp_wait_bar(&acc_empty[abuf], aphase ^ 1u, abort_flag, args.status, kWhereGroupedMma);
+          if (!ok) break;
+        }
+        const uint32_t idesc = C::kIdesc | (static_cast<uint32_t>(tl.n >> 3) << 17);
+        const uint32_t d = tmem_base + static_cast<uint32_t>(abuf * C::kNTile);
+        for (int k = 0; k < tl.red; k += 64) {
+          ok = warp_wait_bar(&full[stage], phase, abort_flag, args.status, kWhereGroupedMma);
+          if (!ok) break;
+          uint8_t* st = smem + static_cast<size_t>(stage) * C::kStageBytes;
+          int steps = 4;
+          if constexpr (Kind == kGroupedDw) {
+            const int live = tl.red - k;
+            if (live < 64) {
+              // the group ends inside this stage: clear the rows behind it up to the next step of 16
+              // (the swizzle permutes 16-byte pieces inside a 128-byte row only, so whole rows are cleared)
+              steps = (live + 15) / 16;
+              const int dead = 16 * steps - live;
+              for (int i = lane; i < 4 * dead * 8; i += 32) {
+                const int box = i / (dead * 8), r = i / 8 % dead, c = i & 7;
+                *reinterpret_cast<uint4*>(st + box * 8192 + (live + r) * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
+          }
+          if constexpr (kRelay) {
+            if (!leader) {
+              if (lane == 0) {
+                const uint32_t bar = in_cta(&peer_full[stage], 0);
+                if (tl.red - k < 64) arrive_in_cluster_release(bar); else arrive_in_cluster(bar);
+              }
+            } else {
+              ok = warp_wait_bar(&peer_full[stage], phase, abort_flag, args.status, kWhereGroupedMma);
+              if (!ok) break;
+            }
+          }
+          if (leader) {
+            tc_fence_after();
+            if (lane == 0) {
+              const uint32_t a = smem_u32(st), b = a + C::kABytes;
+              for (int s = 0; s < steps; ++s) {
+                const uint64_t ad = C::kMnA ? smem_desc_mn_sw128(a + 2048 * s) : smem_desc_sw128(a + 32 * s);
+                const uint64_t bd = C::kMnB ? smem_desc_mn_sw128(b + 2048 * s) : smem_desc_sw128(b + 32 * s);
+                mma_bf16_for<kPair>(d, ad, bd, idesc, (k > 0 || s > 0) ? 1u : 0u);
+              }
+              commit_for<kPair>(&empty[stage]);
+            }
+            __syncwarp();
+          }
+          if (++stage == C::kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        if (leader && lane == 0) commit_for<kPair>(&acc_full[abuf]);
+        abuf ^= 1;
+        if (abuf == 0) aphase ^= 1u;
+      }
+    }
+    // every MMA this thread issued has completed once `drain` flips
+    // (waited on even after an abort: TMEM must not be freed under a running MMA)
+    if (leader && lane == 0) {
+      commit_for<kPair>(drain);
+      drain_mma(drain, args.status);
+    }
+  } else {
+    // ------------------------------------------------------------------ epilogue
+    const int q = warp & 3;               // TMEM lane quarter this warp may access
+    const int g = (warp - 2) >> 2;        // the two groups share the accumulator's columns
+    const int row = 32 * q + lane;        // accumulator row
+    const uint32_t lane_addr = static_cast<uint32_t>(32 * q) << 16;
+    uint8_t* out_row = staging + static_cast<size_t>(threadIdx.x - 64) * C::kOutPitch;
+    const uint32_t empty_bar = kPair ? in_cta(acc_empty, 0) : smem_u32(acc_empty);
+    int abuf = 0;
+    uint32_t aphase = 0;
+    for (int t = first_tile; t < num_tiles; t += stride) {
+      const Tile tl = tile_at<Kind, kPair>(args, off, first, t);
+      const int m = tl.m0 + 128 * rank + row;                // row of the M side
+      const bool live = tl.m0 + 128 * rank + 32 * q < args.m_rows;  // this warp has something to store
+      const uint32_t d = tmem_base + lane_addr + static_cast<uint32_t>(abuf * C::kNTile);
+      if (tl.red > 0) {
+        if (!warp_wait_bar(&acc_full[abuf], aphase, abort_flag, args.status, kWhereGroupedEpilogue)) break;
+        tc_fence_after();
+      }
+      if constexpr (Kind != kGroupedDw) {
+        // a lane holds one output column of every row: a warp stores 32 consecutive columns of a row at once
+        // (64 bytes in bf16, whole sectors)
+        if (live) {
+          const int chunks = (tl.valid + 15) / 16;
+          for (int c = g; c < chunks; c += 2) {
+            float v[16];
+            tmem_ld16(d + 16 * c, v);
+            tmem_wait_ld();
+            const int n = min(16, tl.valid - 16 * c);
+            if (m < args.m_rows) {
+              const long long at = (static_cast<long long>(tl.n0) + 16 * c) * args.ldo + m;
+              if (args.out_f32) {
+                float* o = static_cast<float*>(args.out) + at;
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                  if (i < n) o[i * args.ldo] = v[i];
+              } else {
+                __nv_bfloat16* o = static_cast<__nv_bfloat16*>(args.out) + at;
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                  if (i < n) o[i * args.ldo] = __float2bfloat16_rn(v[i]);
+              }
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_in_cluster(empty_bar + 8 * abuf);
+      } else {
+        // a lane holds a row: 128 bytes of it at a time go through shared memory as one bulk copy
+        constexpr int kCols = C::kNTile / 2;  // columns of this group
+        for (int c = 0; c < kCols; c += 32) {
+          const int col = g * kCols + c;
+          const int width = min(32, tl.valid - col);
+          if (!live || width <= 0) break;
+          float v[32];
+          if (tl.red > 0) {
+            uint32_t u[32];
+            tmem_ld32(d + col, u);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0.f;
+          }
+          // (a group without rows adds nothing to an accumulated gradient)
+          if (m < args.m_rows && !(args.accumulate && tl.red == 0)) {
+            const long long at = (static_cast<long long>(tl.g) * args.m_rows + m) * args.cols + tl.n0 + col;
+            bulk_wait_read_all();  // the previous copy has read the staging row
+            if (args.out_f32) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                reinterpret_cast<float4*>(out_row)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+              fence_proxy_async_smem();
+              float* o = static_cast<float*>(args.out) + at;
+              if (args.accumulate)
+                bulk_add_f32(o, out_row, 4 * width);
+              else
+                bulk_store(o, out_row, 4 * width);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                uint4 u;
+                __nv_bfloat162* h2 = reinterpret_cast<__nv_bfloat162*>(&u);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) h2[j] = __floats2bfloat162_rn(v[8 * i + 2 * j], v[8 * i + 2 * j + 1]);
+                reinterpret_cast<uint4*>(out_row)[i] = u;
+              }
+              fence_proxy_async_smem();
+              bulk_store(static_cast<__nv_bfloat16*>(args.out) + at, out_row, 2 * width);
+            }
+            bulk_commit();
+          }
+        }
+        if (tl.red > 0) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_in_cluster(empty_bar + 8 * abuf);
+        }
+      }
+      if (tl.red > 0) {
+        abuf ^= 1;
+        if (abuf == 0) aphase ^= 1u;
+      }
+    }
+    if constexpr (Kind == kGroupedDw) bulk_wait_all();
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  if constexpr (kPair)
+    cluster_barrier();  // the leader's MMAs read this CTA's shared memory: leave together
+  else
+    __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_free_for<kPair>(tmem_base, C::kTmemCols);
+  }
+}
+
+template <int Kind, bool kPair>
+cudaError_t launch_tiles(const GroupedProblem& p, cudaStream_t s) {
+  using C = Cfg<Kind, kPair>;
+  constexpr auto kern = grouped_bf16_kernel<Kind, kPair>;
+  cudaError_t e = allow_smem<kern>(C::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  Args a{};
+  a.M = p.M;
+  a.G = p.G;
+  a.m_rows = Kind == kGroupedDx ? p.K : p.N;
+  a.m_tiles = (a.m_rows + C::kMTile - 1) / C::kMTile;
+  a.cols = p.K;
+  a.n_tiles = (p.K + C::kNTile - 1) / C::kNTile;
+  a.red = Kind == kGroupedFwd ? p.K : p.N;
+  a.offsets = p.offsets;
+  a.out = p.out;
+  a.ldo = p.ldo;
+  a.out_f32 = p.out_f32;
+  a.accumulate = p.accumulate;
+  a.status = p.status;
+  CUtensorMap tm_a, tm_b, tm_b16;
+  long long tiles;
+  bool ok;
+  if constexpr (Kind == kGroupedDw) {
+    // an empty batch has no rows to map: its tiles load nothing
+    const long long rows = p.M > 0 ? p.M : 1;
+    ok = make_grouped_map(&tm_a, p.M > 0 ? p.a : p.out, 0, rows, p.N, p.M > 0 ? p.lda : p.N, 2, 64) &&
+         make_grouped_map(&tm_b, p.M > 0 ? p.b : p.out, 0, rows, p.K, p.M > 0 ? p.ldb : p.K, 2, 64);
+    tm_b16 = tm_b;
+    tiles = static_cast<long long>(p.G) * a.m_tiles * a.n_tiles;
+  } else {
+    ok = make_grouped_map(&tm_a, p.b, p.G, p.N, p.K, p.K, 2, Kind == kGroupedFwd ? 128 : 64) &&
+         make_grouped_map(&tm_b, p.a, 0, p.M, a.red, p.lda, 2, 64) &&
+         make_grouped_map(&tm_b16, p.a, 0, p.M, a.red, p.lda, 2, 16);
+    tiles = (static_cast<long long>(p.M) / C::kNTile + (p.M < p.G ? p.M : p.G)) * a.m_tiles;
+  }
+  if (!ok) return cudaErrorInvalidValue;
+  if constexpr (kPair) {
+    return launch_pairs<kern>(tiles, C::kSmemBytes, s, tm_a, tm_b, tm_b16, a);
+  } else {
+    const unsigned grid = static_cast<unsigned>(tiles < p.num_sms ? tiles : p.num_sms);
+    return launch_pdl(kern, dim3(grid), dim3(kGroupedThreads), C::kSmemBytes, s, tm_a, tm_b, tm_b16, a);
+  }
+}
+
+template <int Kind>
+cudaError_t dispatch(const GroupedProblem& p, cudaStream_t s) {
+  const long long m = Kind == kGroupedDx ? p.K : p.N;
+  const long long tiles = Kind == kGroupedDw
+                              ? static_cast<long long>(p.G) * ((m + 255) / 256) * ((p.K + 255) / 256)
+                              : (static_cast<long long>(p.M) / 256 + (p.M < p.G ? p.M : p.G)) * ((m + 255) / 256);
+  return tiles >= p.num_sms / 2 ? launch_tiles<Kind, true>(p, s) : launch_tiles<Kind, false>(p, s);
+}
+
+}  // namespace
+
+bool make_grouped_map(CUtensorMap* map, const void* base, int batches, long long rows, long long cols, long long ld,
+                      int elem_bytes, int box_rows) {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  if (fn == nullptr) {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return false;
+    fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  }
+  const CUtensorMapDataType dt = elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                        static_cast<cuuint64_t>(batches)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * elem_bytes,
+                           static_cast<cuuint64_t>(ld) * static_cast<cuuint64_t>(rows) * elem_bytes};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / elem_bytes), static_cast<cuuint32_t>(box_rows), 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = fn(map, dt, batches > 0 ? 3 : 2, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+cudaError_t launch_grouped(const GroupedProblem& p, cudaStream_t stream) {
+  if (p.fp8) return launch_grouped_fp8(p, stream);
+  switch (p.kind) {
+    case kGroupedFwd: return dispatch<kGroupedFwd>(p, stream);
+    case kGroupedDx: return dispatch<kGroupedDx>(p, stream);
+    default: return dispatch<kGroupedDw>(p, stream);
+  }
+}
+
+}  // namespace moe

@@ -39,6 +39,8 @@ SIZES = [
     [0, 1], [1, 0, 2], [0, 0, 0, 3, 0], [16, 17, 15], [130, 0, 1, 260],
     [7] * 20, [64, 1, 64, 200, 33, 0, 0, 5],
 ]
+# enough tiles for the kernels that pair two SMs
+LARGE = [([700, 0, 300, 33, 513, 1000], 2056, 528), ([1, 2048, 31, 257, 256, 255], 2304, 464)]
 SHAPES = [(8, 8), (64, 64), (128, 128), (136, 72), (256, 1024), (264, 328), (1000, 200), (56, 520)]
 
 
@@ -48,7 +50,7 @@ def _cases():
     for i, sizes in enumerate(SIZES):
         for j in (i, i + 3):
             out.append((sizes, *SHAPES[j % len(SHAPES)]))
-    return out
+    return out + LARGE + [(sizes, K, N) for sizes, N, K in LARGE]
 
 
 def _forward(x, w, off, N, M, **kw):
@@ -129,9 +131,9 @@ def test_dw(sizes, N, K, dtype, accumulate):
             assert torch.equal(dw[g], before[g] if accumulate else torch.zeros_like(dw[g]))
 
 
-def test_a_groups_gradient_does_not_see_its_neighbours():
+@pytest.mark.parametrize("N,K", [(136, 72), (1160, 2312)])
+def test_a_groups_gradient_does_not_see_its_neighbours(N, K):
     """NaN in one group's rows stays in that group, for every tail length of a 64-row stage."""
-    N, K = 136, 72
     for n in (1, 15, 16, 17, 48, 63, 64, 65, 100):
         off = offsets_of([n, 40])
         dy, x = _randn(9, n + 40, N), _randn(10, n + 40, K)
