@@ -45,6 +45,7 @@ struct Args {
   void* out;
   long long ldo;     // fwd, dx: elements between rows of out
   int out_f32, accumulate;
+  int wide_a, wide_b;  // an MN-major operand's 128 columns are one box (its row is a multiple of 64 columns)
   int* status;
 };
 
@@ -59,9 +60,8 @@ struct Cfg {
   static constexpr bool kMnA = Kind != kGroupedFwd;
   static constexpr bool kMnB = Kind == kGroupedDw;
   static constexpr int kTmemCols = 2 * kNTile;
-  // dw: each epilogue thread stages 128 bytes of its row for one bulk copy (+ 16: rows spread over the banks)
-  static constexpr int kOutPitch = 144;
-  static constexpr int kOutBytes = Kind == kGroupedDw ? 256 * kOutPitch : 0;
+  // dw: each epilogue warp stages boxes of 32 rows x 128 bytes for TMA stores
+  static constexpr int kOutBytes = Kind == kGroupedDw ? kGroupedEpiWarps * 4096 : 0;
   static constexpr int kStages = (kSmemMax - 1024 - kGroupedReserve - kOutBytes) / kStageBytes;
   static constexpr size_t kSmemBytes =
       static_cast<size_t>(kStages) * kStageBytes + kOutBytes + kGroupedReserve + 1024;
@@ -113,8 +113,8 @@ __device__ __forceinline__ Tile tile_at(const Args& a, const int* off, const int
 
 template <int Kind, bool kPair>
 __global__ void __launch_bounds__(kGroupedThreads, 1)
-    grouped_bf16_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
-                        const __grid_constant__ CUtensorMap tm_b16, const Args args) {
+    grouped_bf16_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ RowMaps tm_b,
+                        const __grid_constant__ CUtensorMap tm_out, const Args args) {
   using C = Cfg<Kind, kPair>;
   // dw in a pair: each CTA counts its own copies, clears its own tail and tells the leader
   constexpr bool kRelay = kPair && Kind == kGroupedDw;
@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tm_a);
-    tma_prefetch_desc(&tm_b);
+    tma_prefetch_desc(&tm_b.map[Kind == kGroupedDw ? 0 : 4]);
   }
   if (warp == 1) tmem_alloc_for<kPair>(tmem_slot, C::kTmemCols);
   pdl_wait();
@@ -179,7 +179,8 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
         const int m0 = tl.m0 + 128 * rank;
         const int half = tl.n / C::kCtas;           // N columns that this CTA loads
         const int n0 = tl.n0 + half * rank;
-        const uint32_t bytes = C::kABytes + half * 128;
+        const int box = row_map_index(half);        // fwd, dx: one box holds them (dw: boxes of 64 columns)
+        const uint32_t bytes = C::kABytes + (Kind == kGroupedDw ? half : row_map_rows(box)) * 128;
         for (int k = 0; k < tl.red; k += 64) {
           if (!wait_bar(&empty[stage], phase ^ 1u, abort_flag, args.status, kWhereGroupedProducer)) {
             ok = false;
@@ -198,19 +199,29 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
           if constexpr (Kind == kGroupedFwd) {
             load_3d<kLead>(a, &tm_a, bar, k, m0, tl.g, pol);
           } else if constexpr (Kind == kGroupedDx) {
-            load_3d<kLead>(a, &tm_a, bar, m0, k, tl.g, pol);
-            load_3d<kLead>(a + 8192, &tm_a, bar, m0 + 64, k, tl.g, pol);
+            if (args.wide_a) {
+              load_4d<kLead>(a, &tm_a, bar, 0, k, m0 >> 6, tl.g, pol);
+            } else {
+              load_3d<kLead>(a, &tm_a, bar, m0, k, tl.g, pol);
+              load_3d<kLead>(a + 8192, &tm_a, bar, m0 + 64, k, tl.g, pol);
+            }
           } else {
-            load_2d<kLead>(a, &tm_a, bar, m0, tl.red0 + k, pol);
-            load_2d<kLead>(a + 8192, &tm_a, bar, m0 + 64, tl.red0 + k, pol);
+            if (args.wide_a) {
+              load_4d<kLead>(a, &tm_a, bar, 0, tl.red0 + k, m0 >> 6, 0, pol);
+            } else {
+              load_3d<kLead>(a, &tm_a, bar, m0, tl.red0 + k, 0, pol);
+              load_3d<kLead>(a + 8192, &tm_a, bar, m0 + 64, tl.red0 + k, 0, pol);
+            }
           }
           if constexpr (Kind == kGroupedDw) {
-            load_2d<kLead>(b, &tm_b, bar, n0, tl.red0 + k, pol);
-            load_2d<kLead>(b + 8192, &tm_b, bar, n0 + 64, tl.red0 + k, pol);
+            if (args.wide_b) {
+              load_4d<kLead>(b, &tm_b.map[0], bar, 0, tl.red0 + k, n0 >> 6, 0, pol);
+            } else {
+              load_3d<kLead>(b, &tm_b.map[0], bar, n0, tl.red0 + k, 0, pol);
+              load_3d<kLead>(b + 8192, &tm_b.map[0], bar, n0 + 64, tl.red0 + k, 0, pol);
+            }
           } else {
-            int r = 0;
-            for (; r + 64 <= half; r += 64) load_2d<kLead>(b + r * 128, &tm_b, bar, k, n0 + r, pol);
-            for (; r < half; r += 16) load_2d<kLead>(b + r * 128, &tm_b16, bar, k, n0 + r, pol);
+            load_2d<kLead>(b, &tm_b.map[box], bar, k, n0, pol);
           }
           ++fills;
           if (++stage == C::kStages) {
@@ -304,7 +315,7 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
     const int g = (warp - 2) >> 2;        // the two groups share the accumulator's columns
     const int row = 32 * q + lane;        // accumulator row
     const uint32_t lane_addr = static_cast<uint32_t>(32 * q) << 16;
-    uint8_t* out_row = staging + static_cast<size_t>(threadIdx.x - 64) * C::kOutPitch;
+    uint8_t* out_box = staging + static_cast<size_t>(warp - 2) * 4096;
     const uint32_t empty_bar = kPair ? in_cta(acc_empty, 0) : smem_u32(acc_empty);
     int abuf = 0;
     uint32_t aphase = 0;
@@ -347,49 +358,54 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
         __syncwarp();
         if (lane == 0) arrive_in_cluster(empty_bar + 8 * abuf);
       } else {
-        // a lane holds a row: 128 bytes of it at a time go through shared memory as one bulk copy
+        // a lane holds a row: 128 bytes of each go through shared memory as one TMA store of the warp's 32 rows
+        // (it leaves out what lies behind the last row and column)
         constexpr int kCols = C::kNTile / 2;  // columns of this group
-        for (int c = 0; c < kCols; c += 32) {
+        const int step = args.out_f32 ? 32 : 64;
+        // a group without rows adds nothing to an accumulated gradient
+        const int end = live && !(args.accumulate && tl.red == 0) ? min(kCols, tl.valid - g * kCols) : 0;
+        for (int c = 0; c < end; c += step) {
           const int col = g * kCols + c;
-          const int width = min(32, tl.valid - col);
-          if (!live || width <= 0) break;
-          float v[32];
-          if (tl.red > 0) {
-            uint32_t u[32];
-            tmem_ld32(d + col, u);
-            tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = 0.f;
-          }
-          // (a group without rows adds nothing to an accumulated gradient)
-          if (m < args.m_rows && !(args.accumulate && tl.red == 0)) {
-            const long long at = (static_cast<long long>(tl.g) * args.m_rows + m) * args.cols + tl.n0 + col;
-            bulk_wait_read_all();  // the previous copy has read the staging row
-            if (args.out_f32) {
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                reinterpret_cast<float4*>(out_row)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-              fence_proxy_async_smem();
-              float* o = static_cast<float*>(args.out) + at;
-              if (args.accumulate)
-                bulk_add_f32(o, out_row, 4 * width);
-              else
-                bulk_store(o, out_row, 4 * width);
+          uint4 piece[8];
+          if (args.out_f32) {
+            uint32_t v[32];
+            if (tl.red > 0) {
+              tmem_ld32(d + col, v);
+              tmem_wait_ld();
             } else {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                uint4 u;
-                __nv_bfloat162* h2 = reinterpret_cast<__nv_bfloat162*>(&u);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) h2[j] = __floats2bfloat162_rn(v[8 * i + 2 * j], v[8 * i + 2 * j + 1]);
-                reinterpret_cast<uint4*>(out_row)[i] = u;
-              }
-              fence_proxy_async_smem();
-              bulk_store(static_cast<__nv_bfloat16*>(args.out) + at, out_row, 2 * width);
+              for (int i = 0; i < 32; ++i) v[i] = 0u;
             }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) piece[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          } else {
+            uint32_t v[64];
+            if (tl.red > 0) {
+              tmem_ld32(d + col, *reinterpret_cast<uint32_t(*)[32]>(v));
+              tmem_ld32(d + col + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+              tmem_wait_ld();
+            } else {
+#pragma unroll
+              for (int i = 0; i < 64; ++i) v[i] = 0u;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float* f = reinterpret_cast<const float*>(v) + 8 * i;
+              piece[i] = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
+                                    pack_bf16(f[6], f[7]));
+            }
+          }
+          if (lane == 0) bulk_wait_read_all();  // the previous store has read the box
+          __syncwarp();
+          stage_row(out_box, lane, piece);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            const int m_first = tl.m0 + 128 * rank + 32 * q;
+            if (args.accumulate)
+              store_3d<true>(&tm_out, out_box, tl.n0 + col, m_first, tl.g);
+            else
+              store_3d<false>(&tm_out, out_box, tl.n0 + col, m_first, tl.g);
             bulk_commit();
           }
         }
@@ -404,7 +420,7 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
         if (abuf == 0) aphase ^= 1u;
       }
     }
-    if constexpr (Kind == kGroupedDw) bulk_wait_all();
+    if (Kind == kGroupedDw && lane == 0) bulk_wait_all();
   }
 
   __syncwarp();
@@ -439,28 +455,36 @@ cudaError_t launch_tiles(const GroupedProblem& p, cudaStream_t s) {
   a.out_f32 = p.out_f32;
   a.accumulate = p.accumulate;
   a.status = p.status;
-  CUtensorMap tm_a, tm_b, tm_b16;
+  CUtensorMap tm_a, tm_out{};
+  RowMaps tm_b;
   long long tiles;
   bool ok;
   if constexpr (Kind == kGroupedDw) {
     // an empty batch has no rows to map: its tiles load nothing
     const long long rows = p.M > 0 ? p.M : 1;
-    ok = make_grouped_map(&tm_a, p.M > 0 ? p.a : p.out, 0, rows, p.N, p.M > 0 ? p.lda : p.N, 2, 64) &&
-         make_grouped_map(&tm_b, p.M > 0 ? p.b : p.out, 0, rows, p.K, p.M > 0 ? p.ldb : p.K, 2, 64);
-    tm_b16 = tm_b;
+    const void* dy = p.M > 0 ? p.a : p.out;
+    const void* x = p.M > 0 ? p.b : p.out;
+    const long long lddy = p.M > 0 ? p.lda : p.N, ldx = p.M > 0 ? p.ldb : p.K;
+    a.wide_a = p.N % 64 == 0;
+    a.wide_b = p.K % 64 == 0;
+    ok = (a.wide_a ? make_wide_map(&tm_a, dy, 1, rows, p.N, lddy) : make_grouped_map(&tm_a, dy, 1, rows, p.N, lddy, 2, 64)) &&
+         (a.wide_b ? make_wide_map(&tm_b.map[0], x, 1, rows, p.K, ldx)
+                   : make_grouped_map(&tm_b.map[0], x, 1, rows, p.K, ldx, 2, 64)) &&
+         make_store_map(&tm_out, p.out, p.G, p.N, p.K, p.K, p.out_f32);
     tiles = static_cast<long long>(p.G) * a.m_tiles * a.n_tiles;
   } else {
-    ok = make_grouped_map(&tm_a, p.b, p.G, p.N, p.K, p.K, 2, Kind == kGroupedFwd ? 128 : 64) &&
-         make_grouped_map(&tm_b, p.a, 0, p.M, a.red, p.lda, 2, 64) &&
-         make_grouped_map(&tm_b16, p.a, 0, p.M, a.red, p.lda, 2, 16);
+    a.wide_a = Kind == kGroupedDx && p.K % 64 == 0;
+    ok = (a.wide_a ? make_wide_map(&tm_a, p.b, p.G, p.N, p.K, p.K)
+                   : make_grouped_map(&tm_a, p.b, p.G, p.N, p.K, p.K, 2, Kind == kGroupedFwd ? 128 : 64)) &&
+         make_row_maps(&tm_b, p.a, p.M, a.red, p.lda, 2);
     tiles = (static_cast<long long>(p.M) / C::kNTile + (p.M < p.G ? p.M : p.G)) * a.m_tiles;
   }
   if (!ok) return cudaErrorInvalidValue;
   if constexpr (kPair) {
-    return launch_pairs<kern>(tiles, C::kSmemBytes, s, tm_a, tm_b, tm_b16, a);
+    return launch_pairs<kern>(tiles, C::kSmemBytes, s, tm_a, tm_b, tm_out, a);
   } else {
     const unsigned grid = static_cast<unsigned>(tiles < p.num_sms ? tiles : p.num_sms);
-    return launch_pdl(kern, dim3(grid), dim3(kGroupedThreads), C::kSmemBytes, s, tm_a, tm_b, tm_b16, a);
+    return launch_pdl(kern, dim3(grid), dim3(kGroupedThreads), C::kSmemBytes, s, tm_a, tm_b, tm_out, a);
   }
 }
 
@@ -475,8 +499,10 @@ cudaError_t dispatch(const GroupedProblem& p, cudaStream_t s) {
 
 }  // namespace
 
-bool make_grouped_map(CUtensorMap* map, const void* base, int batches, long long rows, long long cols, long long ld,
-                      int elem_bytes, int box_rows) {
+namespace {
+
+bool encode(CUtensorMap* map, CUtensorMapDataType type, int dims, const void* base, const cuuint64_t* size,
+            const cuuint64_t* strides, const cuuint32_t* box) {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   if (fn == nullptr) {
     void* p = nullptr;
@@ -486,17 +512,45 @@ bool make_grouped_map(CUtensorMap* map, const void* base, int batches, long long
       return false;
     fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
   }
-  const CUtensorMapDataType dt = elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8;
-  cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
-                        static_cast<cuuint64_t>(batches)};
-  cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * elem_bytes,
-                           static_cast<cuuint64_t>(ld) * static_cast<cuuint64_t>(rows) * elem_bytes};
-  cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / elem_bytes), static_cast<cuuint32_t>(box_rows), 1};
-  cuuint32_t estr[3] = {1, 1, 1};
-  const CUresult r = fn(map, dt, batches > 0 ? 3 : 2, const_cast<void*>(base), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  return fn(map, type, dims, const_cast<void*>(base), size, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+cuuint64_t u64(long long v) { return static_cast<cuuint64_t>(v); }
+
+}  // namespace
+
+bool make_grouped_map(CUtensorMap* map, const void* base, int batches, long long rows, long long cols, long long ld,
+                      int elem_bytes, int box_rows) {
+  const cuuint64_t size[3] = {u64(cols), u64(rows), u64(batches)};
+  const cuuint64_t strides[2] = {u64(ld * elem_bytes), u64(ld * rows * elem_bytes)};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / elem_bytes), static_cast<cuuint32_t>(box_rows), 1};
+  return encode(map, elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8,
+                batches > 0 ? 3 : 2, base, size, strides, box);
+}
+
+bool make_wide_map(CUtensorMap* map, const void* base, int batches, long long rows, long long cols, long long ld) {
+  const cuuint64_t size[4] = {64, u64(rows), u64(cols / 64), u64(batches)};
+  const cuuint64_t strides[3] = {u64(ld * 2), 128, u64(ld * rows * 2)};
+  const cuuint32_t box[4] = {64, 64, 2, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, size, strides, box);
+}
+
+bool make_store_map(CUtensorMap* map, void* base, int batches, long long rows, long long cols, long long ld, bool f32) {
+  const long long elem = f32 ? 4 : 2;
+  const cuuint64_t size[3] = {u64(cols), u64(rows), u64(batches)};
+  const cuuint64_t strides[2] = {u64(ld * elem), u64(ld * rows * elem)};
+  const cuuint32_t box[3] = {f32 ? 32u : 64u, 32, 1};
+  return encode(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, size, strides,
+                box);
+}
+
+bool make_row_maps(RowMaps* maps, const void* base, long long rows, long long cols, long long ld, int elem_bytes) {
+  for (int i = 0; i < 5; ++i)
+    if (!make_grouped_map(&maps->map[i], base, 0, rows, cols, ld, elem_bytes, row_map_rows(i))) return false;
+  return true;
 }
 
 cudaError_t launch_grouped(const GroupedProblem& p, cudaStream_t stream) {

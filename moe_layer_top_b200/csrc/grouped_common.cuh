@@ -137,6 +137,23 @@ __device__ __forceinline__ void load_3d(void* dst, const void* map, uint32_t bar
 }
 
 template <bool kPair>
+__device__ __forceinline__ void load_4d(void* dst, const void* map, uint32_t bar, int x, int y, int z, int w,
+                                        uint64_t policy) {
+  if constexpr (kPair)
+    asm volatile(
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w), "l"(policy)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w), "l"(policy)
+        : "memory");
+}
+
+template <bool kPair>
 __device__ __forceinline__ void tmem_alloc_for(uint32_t* dst_smem, uint32_t ncols) {
   if constexpr (kPair) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst_smem)),
@@ -196,12 +213,32 @@ __device__ __forceinline__ void commit_for(uint64_t* bar) {
     mma_commit(bar);
 }
 
-// fp32 add of `bytes` from shared into global memory (each element one addition)
-__device__ __forceinline__ void bulk_add_f32(void* dst, const void* smem_src, uint32_t bytes) {
-  asm volatile("cp.reduce.async.bulk.global.shared::cta.bulk_group.add.f32 [%0], [%1], %2;" ::"l"(
-                   reinterpret_cast<uint64_t>(dst)),
-               "r"(smem_u32(smem_src)), "r"(bytes)
-               : "memory");
+// TMA tile stores from shared memory (made visible to the async proxy before), tracked by the issuing thread's bulk
+// groups; what lies outside the tensor is not written.  kAdd: fp32 addition to what is there, once per element.
+template <bool kAdd>
+__device__ __forceinline__ void store_3d(const void* map, const void* src, int x, int y, int z) {
+  if constexpr (kAdd)
+    asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+  else
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+
+// Row `lane` of a warp's 32 x 128-byte staging box, as the 128-byte swizzle lays it out: 16-byte piece c goes to
+// c ^ (lane mod 8), so that the lanes of a store spread over all banks.
+__device__ __forceinline__ void stage_row(uint8_t* box, int lane, const uint4 (&piece)[8]) {
+#pragma unroll
+  for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(box + lane * 128 + ((c ^ (lane & 7)) << 4)) = piece[c];
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // Descriptor of an MN-major operand written by TMA with the 128-byte swizzle
@@ -277,10 +314,29 @@ __device__ __forceinline__ int group_of_tile(const int* first, int G, int t) {
 // --------------------------------------------------------------------------
 // host side
 // --------------------------------------------------------------------------
+// tensor map of an output [batches, rows, cols] (bf16 or fp32) for store_3d: boxes of 128 bytes x 32 rows
+bool make_store_map(CUtensorMap* map, void* base, int batches, long long rows, long long cols, long long ld, bool f32);
+
+// tensor map of bf16 [batches, rows, cols] whose box is 64 rows of 2 x 64 columns, the second 64 columns 8192 bytes
+// behind the first (dimensions: column in a run of 64, row, run, batch); cols must be a multiple of 64
+bool make_wide_map(CUtensorMap* map, const void* base, int batches, long long rows, long long cols, long long ld);
+
 // tensor map of [batches, rows, cols] with `ld` elements between rows (rows * ld between batches; batches = 0:
 // two dimensions), box = 128 bytes x box_rows, 128-byte swizzle; what lies outside reads as zero
 bool make_grouped_map(CUtensorMap* map, const void* base, int batches, long long rows, long long cols, long long ld,
                       int elem_bytes, int box_rows);
+
+// Tensor maps of the same rows with boxes of 16, 32, 64, 96 and 128 rows, so that a stage's rows are one TMA
+// instruction: a second and third one for smaller boxes cost more than the rows that a larger box loads in vain
+// (the row loads of 32768 x 1536 over 128 groups: 361 us as boxes of 64 and 16, 255 us as boxes of 128).
+struct RowMaps {
+  CUtensorMap map[5];
+};
+__host__ __device__ constexpr int row_map_index(int rows) {  // the smallest box that holds `rows` (1 .. 128)
+  return rows <= 16 ? 0 : (rows <= 32 ? 1 : (rows <= 64 ? 2 : (rows <= 96 ? 3 : 4)));
+}
+__host__ __device__ constexpr int row_map_rows(int index) { return index == 0 ? 16 : 32 * index; }
+bool make_row_maps(RowMaps* maps, const void* base, long long rows, long long cols, long long ld, int elem_bytes);
 
 // The dynamic shared memory limit is a property of a kernel on each device.
 template <auto kKernel>

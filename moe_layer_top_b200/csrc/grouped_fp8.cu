@@ -12,7 +12,7 @@
 //
 // Row tiles start at any row; a tile that runs past its group's end computes
 // rows of the next group and does not store them; no more rows than the group
-// has are loaded, in boxes of 64 and 16.
+// has are loaded, rounded up to a box of 16, 32, 64, 96 or 128.
 //
 // kPair: a cluster of two CTAs computes 256 x 256 (cta_group::2), 32 KB into
 // each SM per K block; otherwise one CTA computes 128 x 128.
@@ -46,8 +46,7 @@ struct Cfg {
   static constexpr int kAccBufs = kPair ? 2 : 4;
   static constexpr int kTmemCols = kAccBufs * kTile;
   static constexpr int kCols = kTile / 2;              // columns of an epilogue group
-  static constexpr int kOutPitch = 144;                // 128 bytes of a row + 16: rows spread over the banks
-  static constexpr int kOutBytes = 256 * kOutPitch;
+  static constexpr int kOutBytes = kGroupedEpiWarps * 4096;  // a box of 32 rows x 128 bytes per epilogue warp
   static constexpr int kStages = (kSmemMax - 1024 - kGroupedReserve - kOutBytes) / kStageBytes;
   static constexpr size_t kSmemBytes =
       static_cast<size_t>(kStages) * kStageBytes + kOutBytes + kGroupedReserve + 1024;
@@ -74,8 +73,8 @@ __device__ __forceinline__ Tile tile_at(const Args& a, const int* off, const int
 
 template <bool kPair>
 __global__ void __launch_bounds__(kGroupedThreads, 1)
-    grouped_fp8_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_x16,
-                       const __grid_constant__ CUtensorMap tm_w, const Args args) {
+    grouped_fp8_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ CUtensorMap tm_w,
+                       const __grid_constant__ CUtensorMap tm_out, const Args args) {
   using C = Cfg<kPair>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -109,7 +108,7 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
-    tma_prefetch_desc(&tm_x);
+    tma_prefetch_desc(&tm_x.map[4]);
     tma_prefetch_desc(&tm_w);
   }
   if (warp == 1) tmem_alloc_for<kPair>(tmem_slot, C::kTmemCols);
@@ -132,8 +131,12 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
       bool ok = true;
       for (int t = first_tile; t < num_tiles && ok; t += stride) {
         const Tile tl = tile_at<kPair>(args, off, first, t);
-        auto loaded = [&](int r) { return max(0, min(128, (tl.rows - 128 * r + 15) / 16 * 16)); };  // rows of CTA r
+        auto loaded = [&](int r) {  // rows that CTA r loads
+          const int n = min(128, tl.rows - 128 * r);
+          return n > 0 ? row_map_rows(row_map_index(n)) : 0;
+        };
         const int rows = loaded(rank);
+        const CUtensorMap* map = &tm_x.map[rows > 0 ? row_map_index(rows) : 0];
         const uint32_t bytes = kPair ? (loaded(0) + loaded(1)) * 128 + 32768 : rows * 128 + 16384;
         for (int kb = 0; kb < args.k_blocks; ++kb) {
           if (!wait_bar(&empty[stage], phase ^ 1u, abort_flag, args.status, kWhereGroupedProducer)) {
@@ -143,10 +146,7 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
           uint8_t* a = smem + static_cast<size_t>(stage) * C::kStageBytes;
           if (leader) mbar_arrive_expect_tx(&full[stage], bytes);
           const uint32_t bar = kPair ? in_cta(&full[stage], 0) : smem_u32(&full[stage]);
-          const int row0 = tl.row0 + 128 * rank;
-          int r = 0;
-          for (; r + 64 <= rows; r += 64) load_2d<kPair>(a + r * 128, &tm_x, bar, kb * 128, row0 + r, pol);
-          for (; r < rows; r += 16) load_2d<kPair>(a + r * 128, &tm_x16, bar, kb * 128, row0 + r, pol);
+          if (rows > 0) load_2d<kPair>(a, map, bar, kb * 128, tl.row0 + 128 * rank, pol);
           load_3d<kPair>(a + 16384, &tm_w, bar, kb * 128, tl.col0 + 128 * rank, tl.g, pol);
           ++fills;
           if (++stage == C::kStages) {
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
     const int q = warp & 3;               // TMEM lane quarter this warp may access
     const int g = (warp - 2) >> 2;        // column half
     const int row = 32 * q + lane;        // accumulator row
-    uint8_t* out_row = staging + static_cast<size_t>(threadIdx.x - 64) * C::kOutPitch;
+    uint8_t* out_box = staging + static_cast<size_t>(warp - 2) * 4096;
     const uint32_t lane_addr = (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(C::kCols * g);
     const uint32_t empty_bar = kPair ? in_cta(acc_empty, 0) : smem_u32(acc_empty);
     const int kb_n = args.k_blocks;
@@ -256,52 +256,61 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
         }
       }
       if (!ok) break;
-      // store: 128 bytes of the thread's row at a time go through shared memory as one bulk copy
-      if (live && row < rows) {
-        const int width = min(C::kCols, args.N - col);
-        const long long at = grow * args.ldo + col;
-        if (args.out_f32) {
-          float* dst = static_cast<float*>(args.out) + at;
+      if (!live) continue;
+      if (32 * q + 32 <= rows) {
+        // 128 bytes of each row go through shared memory as one TMA store of the warp's 32 rows (it leaves out
+        // what lies behind the last column)
+        const int step = args.out_f32 ? 32 : 64;
 #pragma unroll
-          for (int h = 0; h < C::kCols / 32; ++h) {
-            const int w = min(32, width - 32 * h);
-            if (w > 0) {
-              bulk_wait_read_all();  // the previous copy has read the staging row
+        for (int c = 0; c < C::kCols; c += 32) {
+          if (c % step == 0 && col + c < args.N) {
+            uint4 piece[8];
+            if (args.out_f32) {
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                reinterpret_cast<float4*>(out_row)[i] =
-                    make_float4(acc[32 * h + 4 * i], acc[32 * h + 4 * i + 1], acc[32 * h + 4 * i + 2],
-                                acc[32 * h + 4 * i + 3]);
-              fence_proxy_async_smem();
-              bulk_store(dst + 32 * h, out_row, 4 * w);
+              for (int i = 0; i < 8; ++i) {
+                const float* f = acc + c + 4 * i;
+                piece[i] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                                      __float_as_uint(f[3]));
+              }
+            } else if (c + 64 <= C::kCols) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float* f = acc + (c + 64 <= C::kCols ? c : 0) + 8 * i;
+                piece[i] = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
+                                      pack_bf16(f[6], f[7]));
+              }
+            }
+            if (lane == 0) bulk_wait_read_all();  // the previous store has read the box
+            __syncwarp();
+            stage_row(out_box, lane, piece);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              store_3d<false>(&tm_out, out_box, col + c, tl.row0 + 128 * rank + 32 * q, 0);
               bulk_commit();
             }
           }
-        } else {
-          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(args.out) + at;
+        }
+      } else if (row < rows) {
+        // the group ends inside the warp's rows: each thread stores its own (N is a multiple of 8)
+        const long long at = grow * args.ldo + col;
 #pragma unroll
-          for (int h = 0; h < C::kCols / 64; ++h) {
-            const int w = min(64, width - 64 * h);
-            if (w > 0) {
-              bulk_wait_read_all();
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                uint4 u;
-                __nv_bfloat162* h2 = reinterpret_cast<__nv_bfloat162*>(&u);
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                  h2[j] = __floats2bfloat162_rn(acc[64 * h + 8 * i + 2 * j], acc[64 * h + 8 * i + 2 * j + 1]);
-                reinterpret_cast<uint4*>(out_row)[i] = u;
-              }
-              fence_proxy_async_smem();
-              bulk_store(dst + 64 * h, out_row, 2 * w);
-              bulk_commit();
+        for (int c = 0; c < C::kCols; c += 8) {
+          if (col + c < args.N) {
+            const float* f = acc + c;
+            if (args.out_f32) {
+              float4* o = reinterpret_cast<float4*>(static_cast<float*>(args.out) + at + c);
+              o[0] = make_float4(f[0], f[1], f[2], f[3]);
+              o[1] = make_float4(f[4], f[5], f[6], f[7]);
+            } else {
+              *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(args.out) + at + c) =
+                  make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
             }
           }
         }
       }
     }
-    bulk_wait_all();
+    if (lane == 0) bulk_wait_all();
   }
 
   __syncwarp();
@@ -335,17 +344,18 @@ cudaError_t launch_tiles(const GroupedProblem& p, cudaStream_t s) {
   a.ldo = p.ldo;
   a.out_f32 = p.out_f32;
   a.status = p.status;
-  CUtensorMap tm_x, tm_x16, tm_w;
-  if (!make_grouped_map(&tm_x, p.a, 0, p.M, p.K, p.lda, 1, 64) ||
-      !make_grouped_map(&tm_x16, p.a, 0, p.M, p.K, p.lda, 1, 16) ||
-      !make_grouped_map(&tm_w, p.b, p.G, p.N, p.K, p.K, 1, 128))
+  RowMaps tm_x;
+  CUtensorMap tm_w, tm_out;
+  if (!make_row_maps(&tm_x, p.a, p.M, p.K, p.lda, 1) ||
+      !make_grouped_map(&tm_w, p.b, p.G, p.N, p.K, p.K, 1, 128) ||
+      !make_store_map(&tm_out, p.out, 1, p.M, p.N, p.ldo, p.out_f32))
     return cudaErrorInvalidValue;
   const long long tiles = (static_cast<long long>(p.M) / C::kTile + (p.M < p.G ? p.M : p.G)) * a.n_tiles;
   if constexpr (kPair) {
-    return launch_pairs<kern>(tiles, C::kSmemBytes, s, tm_x, tm_x16, tm_w, a);
+    return launch_pairs<kern>(tiles, C::kSmemBytes, s, tm_x, tm_w, tm_out, a);
   } else {
     const unsigned grid = static_cast<unsigned>(tiles < p.num_sms ? tiles : p.num_sms);
-    return launch_pdl(kern, dim3(grid), dim3(kGroupedThreads), C::kSmemBytes, s, tm_x, tm_x16, tm_w, a);
+    return launch_pdl(kern, dim3(grid), dim3(kGroupedThreads), C::kSmemBytes, s, tm_x, tm_w, tm_out, a);
   }
 }
 
