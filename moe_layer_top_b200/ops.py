@@ -418,20 +418,21 @@ def combine_reduce_scatter_emulated(T, topk, H, ranks, epoch, timeout_us=2_000_0
 _OUT_DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_FP32}
 
 
-def _require(name: str, t, dtype, shape, device, *, rows=False):
+def _require(name: str, t, dtype, shape, device, rows=False):
     """``t`` is a CUDA tensor of this type, shape and device: contiguous, or (``rows``) with unit stride along
     its last dimension."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device and t.is_cuda
+            and (t.is_contiguous() or (rows and t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] == 1)))):
+        return t
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name}: a tensor is needed, got {type(t).__name__}")
     if t.dtype != dtype:
         raise ValueError(f"{name}: type {t.dtype}, {dtype} is needed")
-    if t.device != device or device.type != "cuda":
+    if t.device != device or not t.is_cuda:
         raise ValueError(f"{name}: on {t.device}, needed on the CUDA device of the first argument ({device})")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, {tuple(shape)} is needed")
-    if not t.is_contiguous() and not (rows and t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] == 1)):
-        raise ValueError(f"{name}: " + ("its last dimension must have stride 1" if rows else "must be contiguous"))
-    return t
+    raise ValueError(f"{name}: " + ("its last dimension must have stride 1" if rows else "must be contiguous"))
 
 
 def _2d(name: str, t):
@@ -445,20 +446,30 @@ def _ld(t) -> int:
     return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
 
 
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
 def _run(fn, device, stream, *args):
-    """Call a C entry point on the tensors' device, whichever device is current."""
-    if device.index != torch.cuda.current_device():
+    """Call a C entry point on the tensors' device, whichever device is current.  (These calls are as short as
+    their kernels: addresses go as plain numbers and the stream is read as one.)"""
+    index = device.index
+    if index != torch._C._cuda_getDevice():
         with torch.cuda.device(device):
             return _run(fn, device, stream, *args)
-    s = torch.cuda.current_stream(device) if stream is None else stream
-    _check(fn(*args, ctypes.c_void_p(s.cuda_stream)))
+    _check(fn(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream))
 
 
 def _out(name, out, shape, dtype, device):
     """``out`` checked, or a new tensor."""
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    return _require(name, out, dtype, shape, device, rows=True)
+        return torch.empty(*shape, dtype=dtype, device=device)
+    return _require(name, out, dtype, shape, device, True)
+
+
+def _like(x, dtype=None):
+    """A new contiguous tensor of x's shape (the cheapest of torch's allocating calls)."""
+    return torch.empty_like(x, dtype=dtype, memory_format=torch.contiguous_format)
 
 
 def _out_dtype(out, out_dtype):
@@ -479,23 +490,24 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, *, residu
     [ceil(H / 128), T]) and ``rstd`` (fp32 [T] if asked for)."""
     T, H = _2d("x", x)
     dev = x.device
-    _require("x", x, torch.bfloat16, (T, H), dev, rows=True)
+    _require("x", x, torch.bfloat16, (T, H), dev, True)
     _require("weight", weight, torch.bfloat16, (H,), dev)
     if residual is not None:
-        _require("residual", residual, torch.bfloat16, (T, H), dev, rows=True)
-        residual_out = _out("residual_out", residual_out, (T, H), torch.bfloat16, dev)
+        _require("residual", residual, torch.bfloat16, (T, H), dev, True)
+        residual_out = _like(x) if residual_out is None else _require("residual_out", residual_out, torch.bfloat16,
+                                                                       (T, H), dev, True)
     elif residual_out is not None:
         raise ValueError("residual_out: given without residual")
     if y is True or y is False or y is None:
-        y = torch.empty((T, H), dtype=torch.bfloat16, device=dev) if y else None
+        y = _like(x) if y else None
     else:
-        _require("y", y, torch.bfloat16, (T, H), dev, rows=True)
-    codes = torch.empty((T, H), dtype=torch.uint8, device=dev) if fp8 else None
-    scales = torch.empty(((H + 127) // 128, T), dtype=torch.float32, device=dev) if fp8 else None
-    r = torch.empty((T,), dtype=torch.float32, device=dev) if rstd else None
-    _run(lib().moe_rms_norm, dev, stream, _ptr(x), _ld(x), _ptr(residual), 0 if residual is None else _ld(residual),
-         _ptr(residual_out), 0 if residual is None else _ld(residual_out), _ptr(weight), eps, T, H, _ptr(y),
-         0 if y is None else _ld(y), _ptr(codes), _ptr(scales), _ptr(r))
+        _require("y", y, torch.bfloat16, (T, H), dev, True)
+    codes = _like(x, torch.uint8) if fp8 else None
+    scales = x.new_empty(((H + 127) // 128, T), dtype=torch.float32) if fp8 else None
+    r = x.new_empty(T, dtype=torch.float32) if rstd else None
+    _run(lib().moe_rms_norm, dev, stream, _addr(x), _ld(x), _addr(residual), 0 if residual is None else _ld(residual),
+         _addr(residual_out), 0 if residual is None else _ld(residual_out), _addr(weight), eps, T, H, _addr(y),
+         0 if y is None else _ld(y), _addr(codes), _addr(scales), _addr(r))
     return {"residual": residual_out, "y": y, "codes": codes, "scales": scales, "rstd": r}
 
 
@@ -508,21 +520,20 @@ def rms_norm_backward(dy: torch.Tensor, s: torch.Tensor, weight: torch.Tensor, r
     ``moe_rms_norm_backward_workspace_size`` bytes (allocated if not given)."""
     T, H = _2d("dy", dy)
     dev = dy.device
-    _require("dy", dy, torch.bfloat16, (T, H), dev, rows=True)
-    _require("s", s, torch.bfloat16, (T, H), dev, rows=True)
+    _require("dy", dy, torch.bfloat16, (T, H), dev, True)
+    _require("s", s, torch.bfloat16, (T, H), dev, True)
     _require("weight", weight, torch.bfloat16, (H,), dev)
     _require("rstd", rstd, torch.float32, (T,), dev)
     if dresidual is not None:
-        _require("dresidual", dresidual, torch.bfloat16, (T, H), dev, rows=True)
-    dx = _out("dx", dx, (T, H), torch.bfloat16, dev)
-    dweight = torch.empty((H,), dtype=torch.float32, device=dev)
+        _require("dresidual", dresidual, torch.bfloat16, (T, H), dev, True)
+    dx = _like(dy) if dx is None else _require("dx", dx, torch.bfloat16, (T, H), dev, True)
+    dweight = dy.new_empty(H, dtype=torch.float32)
     if ws is None:
-        ws = torch.empty((max(int(lib().moe_rms_norm_backward_workspace_size(T, H)), 16),), dtype=torch.uint8,
-                         device=dev)
+        ws = dy.new_empty(max(int(lib().moe_rms_norm_backward_workspace_size(T, H)), 16), dtype=torch.uint8)
     else:
         _require("ws", ws, torch.uint8, ws.shape, dev)
-    _run(lib().moe_rms_norm_backward, dev, stream, _ptr(dy), _ld(dy), _ptr(s), _ld(s), _ptr(weight), _ptr(rstd),
-         _ptr(dresidual), 0 if dresidual is None else _ld(dresidual), T, H, _ptr(dx), _ld(dx), _ptr(dweight), _ptr(ws),
+    _run(lib().moe_rms_norm_backward, dev, stream, _addr(dy), _ld(dy), _addr(s), _ld(s), _addr(weight), _addr(rstd),
+         _addr(dresidual), 0 if dresidual is None else _ld(dresidual), T, H, _addr(dx), _ld(dx), _addr(dweight), _addr(ws),
          ws.numel())
     return dx, dweight
 
@@ -530,10 +541,10 @@ def rms_norm_backward(dy: torch.Tensor, s: torch.Tensor, weight: torch.Tensor, r
 def quantize_rows_fp8(x: torch.Tensor, stream=None):
     """bf16 [rows, cols] -> FP8 rows: (E4M3 codes as uint8 [rows, cols], fp32 scales [ceil(cols / 128), rows])."""
     rows, cols = _2d("x", x)
-    _require("x", x, torch.bfloat16, (rows, cols), x.device, rows=True)
-    codes = torch.empty((rows, cols), dtype=torch.uint8, device=x.device)
-    scales = torch.empty(((cols + 127) // 128, rows), dtype=torch.float32, device=x.device)
-    _run(lib().moe_quantize_rows_fp8, x.device, stream, _ptr(x), _ld(x), rows, cols, _ptr(codes), _ptr(scales))
+    _require("x", x, torch.bfloat16, (rows, cols), x.device, True)
+    codes = _like(x, torch.uint8)
+    scales = x.new_empty(((cols + 127) // 128, rows), dtype=torch.float32)
+    _run(lib().moe_quantize_rows_fp8, x.device, stream, _addr(x), _ld(x), rows, cols, _addr(codes), _addr(scales))
     return codes, scales
 
 
@@ -543,8 +554,8 @@ def dequantize_rows_fp8(codes: torch.Tensor, scales: torch.Tensor, *, out=None, 
     dev = codes.device
     _require("codes", codes, torch.uint8, (rows, cols), dev)
     _require("scales", scales, torch.float32, ((cols + 127) // 128, rows), dev)
-    out = _out("out", out, (rows, cols), torch.bfloat16, dev)
-    _run(lib().moe_dequantize_rows_fp8, dev, stream, _ptr(codes), _ptr(scales), rows, cols, _ptr(out), _ld(out))
+    out = _like(codes, torch.bfloat16) if out is None else _require("out", out, torch.bfloat16, (rows, cols), dev, True)
+    _run(lib().moe_dequantize_rows_fp8, dev, stream, _addr(codes), _addr(scales), rows, cols, _addr(out), _ld(out))
     return out
 
 
@@ -575,13 +586,13 @@ def matmul_fp8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale:
     _require("w_scale", w_scale, torch.float32, ((N + 127) // 128, (K + 127) // 128), dev)
     dtype = _out_dtype(out, out_dtype)
     out = _out("out", out, (M, N), dtype, dev)
-    _run(lib().moe_matmul_fp8, dev, stream, _ptr(x), _ptr(x_scale), _ptr(w), _ptr(w_scale), M, N, K, _ptr(out),
-         _ld(out), _OUT_DTYPES[dtype], _status_ptr(status, dev))
+    _run(lib().moe_matmul_fp8, dev, stream, _addr(x), _addr(x_scale), _addr(w), _addr(w_scale), M, N, K, _addr(out),
+         _ld(out), _OUT_DTYPES[dtype], _status(status, dev))
     return out
 
 
-def _status_ptr(status, dev):
-    return None if status is None else _ptr(_require("status", status, torch.int32, (1,), dev))
+def _status(status, dev):
+    return None if status is None else _addr(_require("status", status, torch.int32, (1,), dev))
 
 
 def grouped_matmul(x: torch.Tensor, w: torch.Tensor, offsets, *, x_scale=None, w_scale=None, out=None, out_dtype=None,
@@ -598,18 +609,18 @@ def grouped_matmul(x: torch.Tensor, w: torch.Tensor, offsets, *, x_scale=None, w
     fp8 = x_scale is not None
     G, N, _ = _weight("w", w, torch.uint8 if fp8 else torch.bfloat16, dev)
     _require("w", w, w.dtype, (G, N, K), dev)
-    _require("x", x, torch.uint8 if fp8 else torch.bfloat16, (M, K), dev, rows=not fp8)
+    _require("x", x, torch.uint8 if fp8 else torch.bfloat16, (M, K), dev, not fp8)
     _offsets(offsets, G, dev)
     dtype = _out_dtype(out, out_dtype)
     out = _out("out", out, (M, N), dtype, dev)
     if fp8:
         _require("x_scale", x_scale, torch.float32, ((K + 127) // 128, M), dev)
         _require("w_scale", w_scale, torch.float32, (G, (N + 127) // 128, (K + 127) // 128), dev)
-        _run(lib().moe_grouped_matmul_fp8, dev, stream, _ptr(x), _ptr(x_scale), _ptr(w), _ptr(w_scale), _ptr(offsets),
-             M, G, N, K, _ptr(out), _ld(out), _OUT_DTYPES[dtype], _status_ptr(status, dev))
+        _run(lib().moe_grouped_matmul_fp8, dev, stream, _addr(x), _addr(x_scale), _addr(w), _addr(w_scale), _addr(offsets),
+             M, G, N, K, _addr(out), _ld(out), _OUT_DTYPES[dtype], _status(status, dev))
     else:
-        _run(lib().moe_grouped_matmul, dev, stream, _ptr(x), _ld(x), _ptr(w), _ptr(offsets), M, G, N, K, _ptr(out),
-             _ld(out), _OUT_DTYPES[dtype], _status_ptr(status, dev))
+        _run(lib().moe_grouped_matmul, dev, stream, _addr(x), _ld(x), _addr(w), _addr(offsets), M, G, N, K, _addr(out),
+             _ld(out), _OUT_DTYPES[dtype], _status(status, dev))
     return out
 
 
@@ -620,12 +631,12 @@ def grouped_matmul_dx(dy: torch.Tensor, w: torch.Tensor, offsets, *, out=None, o
     dev = dy.device
     G, _, K = _weight("w", w, torch.bfloat16, dev)
     _require("w", w, torch.bfloat16, (G, N, K), dev)
-    _require("dy", dy, torch.bfloat16, (M, N), dev, rows=True)
+    _require("dy", dy, torch.bfloat16, (M, N), dev, True)
     _offsets(offsets, G, dev)
     dtype = _out_dtype(out, out_dtype)
     out = _out("out", out, (M, K), dtype, dev)
-    _run(lib().moe_grouped_matmul_dx, dev, stream, _ptr(dy), _ld(dy), _ptr(w), _ptr(offsets), M, G, N, K, _ptr(out),
-         _ld(out), _OUT_DTYPES[dtype], _status_ptr(status, dev))
+    _run(lib().moe_grouped_matmul_dx, dev, stream, _addr(dy), _ld(dy), _addr(w), _addr(offsets), M, G, N, K, _addr(out),
+         _ld(out), _OUT_DTYPES[dtype], _status(status, dev))
     return out
 
 
@@ -636,17 +647,17 @@ def grouped_matmul_dw(dy: torch.Tensor, x: torch.Tensor, offsets, *, out=None, o
     M, N = _2d("dy", dy)
     K = _2d("x", x)[1]
     dev = dy.device
-    _require("dy", dy, torch.bfloat16, (M, N), dev, rows=True)
-    _require("x", x, torch.bfloat16, (M, K), dev, rows=True)
+    _require("dy", dy, torch.bfloat16, (M, N), dev, True)
+    _require("x", x, torch.bfloat16, (M, K), dev, True)
     G = 1 if offsets is None else offsets.numel() - 1
     _offsets(offsets, G, dev)
     if accumulate and out is None:
         raise ValueError("accumulate: needs out")
     dtype = _out_dtype(out, out_dtype)
     if out is None:
-        out = torch.empty((G, N, K), dtype=dtype, device=dev)
+        out = torch.empty(G, N, K, dtype=dtype, device=dev)
     else:
         _require("out", out, dtype, (G, N, K), dev)
-    _run(lib().moe_grouped_matmul_dw, dev, stream, _ptr(dy), _ld(dy), _ptr(x), _ld(x), _ptr(offsets), M, G, N, K,
-         _ptr(out), _OUT_DTYPES[dtype], 1 if accumulate else 0, _status_ptr(status, dev))
+    _run(lib().moe_grouped_matmul_dw, dev, stream, _addr(dy), _ld(dy), _addr(x), _ld(x), _addr(offsets), M, G, N, K,
+         _addr(out), _OUT_DTYPES[dtype], 1 if accumulate else 0, _status(status, dev))
     return out
