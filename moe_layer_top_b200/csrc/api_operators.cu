@@ -134,7 +134,7 @@ int moe_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr, 
 
 size_t moe_rms_norm_backward_workspace_size(int32_t T, int32_t H) {
   if (check_norm_shape("rms_norm_backward", T, H) != MOE_OK) return 0;
-  return static_cast<size_t>(moe::rms_norm_backward_blocks(T)) * static_cast<size_t>(H) * sizeof(float);
+  return static_cast<size_t>(moe::rms_norm_backward_blocks(T, H)) * static_cast<size_t>(H) * sizeof(float);
 }
 
 int moe_rms_norm_backward(const void* dy, int64_t lddy, const void* s, int64_t lds, const void* weight,
@@ -152,7 +152,7 @@ int moe_rms_norm_backward(const void* dy, int64_t lddy, const void* s, int64_t l
     if (!rstd || !aligned(rstd, 4)) return api_fail(MOE_ERR_INVALID, "%s: rstd is required, 4-byte aligned", what);
     if (!ws || !aligned(ws, 16)) return api_fail(MOE_ERR_INVALID, "%s: ws is required, 16-byte aligned", what);
   }
-  const int blocks = moe::rms_norm_backward_blocks(T);
+  const int blocks = moe::rms_norm_backward_blocks(T, H);
   const size_t need = static_cast<size_t>(blocks) * static_cast<size_t>(H) * sizeof(float);
   if (ws_bytes < need)
     return api_fail(MOE_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", what, ws_bytes, need);

@@ -22,10 +22,14 @@
 // kPair: a cluster of two CTAs computes a 256 x 256 tile (cta_group::2): each
 // SM loads 128 of the 256 A rows and half of the B rows, so a stage moves 32 KB
 // into an SM for 512 cycles of MMA, which the shared-memory port keeps up with
-// (a 128 x 256 tile of one SM needs 48 KB).  Without kPair one CTA computes
+// (a 128 x 256 tile of one SM needs 48 KB).  kSingle: one CTA computes
 // 128 x 128: more and smaller tiles for small problems.
 //
-// Persistent, 10 warps per CTA: TMA producer, MMA issuer (of the leader CTA),
+// kSplit: a cluster of up to eight CTAs shares the reduction of one 128 x 128
+// tile, each leaves its partial sums in shared memory and all add a part of
+// them up, in rank order: where tiles are few, all SMs stream operands.
+//
+// Persistent (kSplit: one tile per cluster), 10 warps per CTA: TMA producer, MMA issuer (of the leader CTA),
 // eight epilogue warps; the accumulator is double-buffered in TMEM, so a
 // tile's stores run under the next tile's products.
 #include "grouped_common.cuh"
@@ -44,13 +48,17 @@ struct Args {
   const int32_t* offsets;
   void* out;
   long long ldo;     // fwd, dx: elements between rows of out
+  int splits;        // kModeSplit: CTAs per cluster
   int out_f32, accumulate;
   int wide_a, wide_b;  // an MN-major operand's 128 columns are one box (its row is a multiple of 64 columns)
   int* status;
 };
 
-template <int Kind, bool kPair>
+constexpr int kThreads = 320;
+
+template <int Kind, int Mode>
 struct Cfg {
+  static constexpr bool kPair = Mode == kModePair;
   static constexpr int kCtas = kPair ? 2 : 1;
   static constexpr int kMTile = 128 * kCtas;
   static constexpr int kNTile = 128 * kCtas;           // most N columns of a tile
@@ -61,13 +69,14 @@ struct Cfg {
   static constexpr bool kMnB = Kind == kGroupedDw;
   static constexpr int kTmemCols = 2 * kNTile;
   // dw: each epilogue warp stages boxes of 32 rows x 128 bytes for TMA stores
-  static constexpr int kOutBytes = Kind == kGroupedDw ? kGroupedEpiWarps * 4096 : 0;
+  static constexpr int kOutBytes = Kind == kGroupedDw && Mode != kModeSplit ? kGroupedEpiWarps * 4096 : 0;
   static constexpr int kStages = (kSmemMax - 1024 - kGroupedReserve - kOutBytes) / kStageBytes;
   static constexpr size_t kSmemBytes =
       static_cast<size_t>(kStages) * kStageBytes + kOutBytes + kGroupedReserve + 1024;
   static constexpr uint32_t kIdesc =
       make_idesc(kMTile, 0, false) | (kMnA ? 1u << 15 : 0u) | (kMnB ? 1u << 16 : 0u);
   static_assert(kStages >= 4 && kStages <= 16, "ring depth");
+  static_assert(kStages * kStageBytes >= 128 * kPartialPitch * 4, "partial sums fit the ring");
 };
 
 struct Tile {
@@ -78,9 +87,9 @@ struct Tile {
   int red0, red;  // dw: the group's first row and row count; otherwise 0 and the reduction length
 };
 
-template <int Kind, bool kPair>
+template <int Kind, int Mode>
 __device__ __forceinline__ Tile tile_at(const Args& a, const int* off, const int* first, int t) {
-  using C = Cfg<Kind, kPair>;
+  using C = Cfg<Kind, Mode>;
   Tile r;
   if constexpr (Kind == kGroupedDw) {
     const int per_group = a.m_tiles * a.n_tiles;
@@ -111,11 +120,12 @@ __device__ __forceinline__ Tile tile_at(const Args& a, const int* off, const int
   return r;
 }
 
-template <int Kind, bool kPair>
-__global__ void __launch_bounds__(kGroupedThreads, 1)
+template <int Kind, int Mode>
+__global__ void __launch_bounds__(kThreads, 1)
     grouped_bf16_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ RowMaps tm_b,
                         const __grid_constant__ CUtensorMap tm_out, const Args args) {
-  using C = Cfg<Kind, kPair>;
+  using C = Cfg<Kind, Mode>;
+  constexpr bool kPair = C::kPair, kSplit = Mode == kModeSplit;
   // dw in a pair: each CTA counts its own copies, clears its own tail and tells the leader
   constexpr bool kRelay = kPair && Kind == kGroupedDw;
   extern __shared__ uint8_t smem_raw[];
@@ -136,7 +146,8 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
   static_assert((3 * C::kStages + 5) * 8 + 8 <= 640, "barriers overlap the scan buffer");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = kPair ? static_cast<int>(cluster_rank()) : 0;
+  const int cta = kPair || kSplit ? static_cast<int>(cluster_rank()) : 0;  // rank in the cluster
+  const int rank = kPair ? cta : 0;                                        // half of the tile
   const bool leader = rank == 0;
   pdl_launch_dependents();
   if (threadIdx.x == 0) {
@@ -158,13 +169,20 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
   if (warp == 1) tmem_alloc_for<kPair>(tmem_slot, C::kTmemCols);
   pdl_wait();
   tc_fence_before();
-  int num_tiles = build_group_tables(args.offsets, args.M, args.G, C::kNTile, args.m_tiles, off,
-                                     Kind == kGroupedDw ? nullptr : first, scan);
+  int num_tiles = build_group_tables<kThreads>(args.offsets, args.M, args.G, C::kNTile, args.m_tiles, off,
+                                               Kind == kGroupedDw ? nullptr : first, scan);
   if constexpr (Kind == kGroupedDw) num_tiles = args.G * args.m_tiles * args.n_tiles;
   if constexpr (kPair) cluster_barrier();  // the peer's barriers are initialised before any remote arrival
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const int first_tile = static_cast<int>(blockIdx.x) / C::kCtas, stride = static_cast<int>(gridDim.x) / C::kCtas;
+  const int cluster_size = kSplit ? args.splits : C::kCtas;
+  const int first_tile = static_cast<int>(blockIdx.x) / cluster_size;
+  const int stride = static_cast<int>(gridDim.x) / cluster_size;  // kSplit: no cluster takes a second tile
+  // the part of a tile's reduction that this CTA takes
+  auto red_begin = [&](const Tile& tl) { return kSplit ? (tl.red + 63) / 64 * cta / args.splits * 64 : 0; };
+  auto red_end = [&](const Tile& tl) {
+    return kSplit ? min(tl.red, (tl.red + 63) / 64 * (cta + 1) / args.splits * 64) : tl.red;
+  };
 
   if (warp == 0) {
     // ------------------------------------------------------------------ producer (of each CTA)
@@ -175,13 +193,14 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
       long long fills = 0;
       bool ok = true;
       for (int t = first_tile; t < num_tiles && ok; t += stride) {
-        const Tile tl = tile_at<Kind, kPair>(args, off, first, t);
+        const Tile tl = tile_at<Kind, Mode>(args, off, first, t);
         const int m0 = tl.m0 + 128 * rank;
         const int half = tl.n / C::kCtas;           // N columns that this CTA loads
         const int n0 = tl.n0 + half * rank;
         const int box = row_map_index(half);        // fwd, dx: one box holds them (dw: boxes of 64 columns)
         const uint32_t bytes = C::kABytes + (Kind == kGroupedDw ? half : row_map_rows(box)) * 128;
-        for (int k = 0; k < tl.red; k += 64) {
+        const int k1 = red_end(tl);
+        for (int k = red_begin(tl); k < k1; k += 64) {
           if (!wait_bar(&empty[stage], phase ^ 1u, abort_flag, args.status, kWhereGroupedProducer)) {
             ok = false;
             break;
@@ -240,15 +259,16 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
     bool ok = true;
     if (leader || kRelay) {
       for (int t = first_tile; t < num_tiles && ok; t += stride) {
-        const Tile tl = tile_at<Kind, kPair>(args, off, first, t);
-        if (tl.red == 0) continue;
+        const Tile tl = tile_at<Kind, Mode>(args, off, first, t);
+        const int k0 = red_begin(tl), k1 = red_end(tl);
+        if (k0 >= k1) continue;
         if (leader) {
           ok = warp_wait_bar(&acc_empty[abuf], aphase ^ 1u, abort_flag, args.status, kWhereGroupedMma);
           if (!ok) break;
         }
         const uint32_t idesc = C::kIdesc | (static_cast<uint32_t>(tl.n >> 3) << 17);
         const uint32_t d = tmem_base + static_cast<uint32_t>(abuf * C::kNTile);
-        for (int k = 0; k < tl.red; k += 64) {
+        for (int k = k0; k < k1; k += 64) {
           ok = warp_wait_bar(&full[stage], phase, abort_flag, args.status, kWhereGroupedMma);
           if (!ok) break;
           uint8_t* st = smem + static_cast<size_t>(stage) * C::kStageBytes;
@@ -286,7 +306,7 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
               for (int s = 0; s < steps; ++s) {
                 const uint64_t ad = C::kMnA ? smem_desc_mn_sw128(a + 2048 * s) : smem_desc_sw128(a + 32 * s);
                 const uint64_t bd = C::kMnB ? smem_desc_mn_sw128(b + 2048 * s) : smem_desc_sw128(b + 32 * s);
-                mma_bf16_for<kPair>(d, ad, bd, idesc, (k > 0 || s > 0) ? 1u : 0u);
+                mma_bf16_for<kPair>(d, ad, bd, idesc, (k > k0 || s > 0) ? 1u : 0u);
               }
               commit_for<kPair>(&empty[stage]);
             }
@@ -320,11 +340,12 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
     int abuf = 0;
     uint32_t aphase = 0;
     for (int t = first_tile; t < num_tiles; t += stride) {
-      const Tile tl = tile_at<Kind, kPair>(args, off, first, t);
+      const Tile tl = tile_at<Kind, Mode>(args, off, first, t);
       const int m = tl.m0 + 128 * rank + row;                // row of the M side
       const bool live = tl.m0 + 128 * rank + 32 * q < args.m_rows;  // this warp has something to store
       const uint32_t d = tmem_base + lane_addr + static_cast<uint32_t>(abuf * C::kNTile);
-      if (tl.red > 0) {
+      const bool any = red_begin(tl) < red_end(tl);  // otherwise there is no accumulator: zeros
+      if (any) {
         if (!warp_wait_bar(&acc_full[abuf], aphase, abort_flag, args.status, kWhereGroupedEpilogue)) break;
         tc_fence_after();
       }
@@ -335,10 +356,24 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
           const int chunks = (tl.valid + 15) / 16;
           for (int c = g; c < chunks; c += 2) {
             float v[16];
-            tmem_ld16(d + 16 * c, v);
-            tmem_wait_ld();
+            if (any) {
+              uint32_t u[16];
+              tmem_ld16u(d + 16 * c, u);
+              tmem_wait_ld();
+              pin16(u);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(u[i]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] = 0.f;
+            }
             const int n = min(16, tl.valid - 16 * c);
-            if (m < args.m_rows) {
+            if constexpr (kSplit) {
+              // this CTA's share of the sums, for all CTAs of the cluster (the ring is idle: its last MMA is done)
+              float* p = reinterpret_cast<float*>(smem) + 16 * c * kPartialPitch + row;
+#pragma unroll
+              for (int i = 0; i < 16; ++i) p[i * kPartialPitch] = v[i];
+            } else if (m < args.m_rows) {
               const long long at = (static_cast<long long>(tl.n0) + 16 * c) * args.ldo + m;
               if (args.out_f32) {
                 float* o = static_cast<float*>(args.out) + at;
@@ -354,9 +389,11 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
             }
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) arrive_in_cluster(empty_bar + 8 * abuf);
+        if (any) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_in_cluster(empty_bar + 8 * abuf);
+        }
       } else {
         // a lane holds a row: 128 bytes of each go through shared memory as one TMA store of the warp's 32 rows
         // (it leaves out what lies behind the last row and column)
@@ -364,14 +401,33 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
         const int step = args.out_f32 ? 32 : 64;
         // a group without rows adds nothing to an accumulated gradient
         const int end = live && !(args.accumulate && tl.red == 0) ? min(kCols, tl.valid - g * kCols) : 0;
-        for (int c = 0; c < end; c += step) {
+        if constexpr (kSplit) {
+#pragma unroll
+          for (int c = 0; c < kCols; c += 32) {
+            if (c >= end) break;
+            uint32_t v[32];
+            if (any) {
+              tmem_ld32(d + g * kCols + c, v);
+              tmem_wait_ld();
+              pin32(v);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = 0u;
+            }
+            uint4* p = reinterpret_cast<uint4*>(reinterpret_cast<float*>(smem) + row * kPartialPitch + g * kCols + c);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) p[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          }
+        }
+        for (int c = 0; !kSplit && c < end; c += step) {
           const int col = g * kCols + c;
           uint4 piece[8];
           if (args.out_f32) {
             uint32_t v[32];
-            if (tl.red > 0) {
+            if (any) {
               tmem_ld32(d + col, v);
               tmem_wait_ld();
+              pin32(v);
             } else {
 #pragma unroll
               for (int i = 0; i < 32; ++i) v[i] = 0u;
@@ -379,20 +435,23 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
 #pragma unroll
             for (int i = 0; i < 8; ++i) piece[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
           } else {
-            uint32_t v[64];
-            if (tl.red > 0) {
-              tmem_ld32(d + col, *reinterpret_cast<uint32_t(*)[32]>(v));
-              tmem_ld32(d + col + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+            uint32_t v[2][32];
+            if (any) {
+              tmem_ld32(d + col, v[0]);
+              tmem_ld32(d + col + 32, v[1]);
               tmem_wait_ld();
+              pin32(v[0]);
+              pin32(v[1]);
             } else {
 #pragma unroll
-              for (int i = 0; i < 64; ++i) v[i] = 0u;
+              for (int i = 0; i < 32; ++i) v[0][i] = v[1][i] = 0u;
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              const float* f = reinterpret_cast<const float*>(v) + 8 * i;
-              piece[i] = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
-                                    pack_bf16(f[6], f[7]));
+              float f[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(v[i / 4][8 * (i & 3) + j]);
+              piece[i] = pack_bf16x8(f);
             }
           }
           if (lane == 0) bulk_wait_read_all();  // the previous store has read the box
@@ -409,37 +468,53 @@ __global__ void __launch_bounds__(kGroupedThreads, 1)
             bulk_commit();
           }
         }
-        if (tl.red > 0) {
+        if (any) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) arrive_in_cluster(empty_bar + 8 * abuf);
         }
       }
-      if (tl.red > 0) {
+      if (any) {
         abuf ^= 1;
         if (abuf == 0) aphase ^= 1u;
       }
     }
-    if (Kind == kGroupedDw && lane == 0) bulk_wait_all();
+    if (Kind == kGroupedDw && !kSplit && lane == 0) bulk_wait_all();
   }
 
   __syncwarp();
   tc_fence_before();
-  if constexpr (kPair)
+  if constexpr (kSplit) {
+    cluster_barrier();  // every CTA's partial sums are written
+    if (first_tile < num_tiles) {
+      const Tile tl = tile_at<Kind, Mode>(args, off, first, first_tile);
+      if constexpr (Kind == kGroupedDw) {
+        if (!(args.accumulate && tl.red == 0))
+          add_partials<kThreads>(smem, cta, args.splits, min(128, args.m_rows - tl.m0), tl.valid, args.out,
+                                 (static_cast<long long>(tl.g) * args.m_rows + tl.m0) * args.cols + tl.n0, args.cols,
+                                 args.out_f32, args.accumulate);
+      } else {
+        add_partials<kThreads>(smem, cta, args.splits, tl.valid, min(128, args.m_rows - tl.m0), args.out,
+                               static_cast<long long>(tl.n0) * args.ldo + tl.m0, args.ldo, args.out_f32, false);
+      }
+    }
+    cluster_barrier();  // no CTA leaves before the others have read its sums
+  } else if constexpr (kPair) {
     cluster_barrier();  // the leader's MMAs read this CTA's shared memory: leave together
-  else
+  } else {
     __syncthreads();
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_free_for<kPair>(tmem_base, C::kTmemCols);
   }
 }
 
-template <int Kind, bool kPair>
-cudaError_t launch_tiles(const GroupedProblem& p, cudaStream_t s) {
-  using C = Cfg<Kind, kPair>;
-  constexpr auto kern = grouped_bf16_kernel<Kind, kPair>;
-  cudaError_t e = allow_smem<kern>(C::kSmemBytes);
+template <int Kind, int Mode>
+cudaError_t launch_tiles(const GroupedProblem& p, int splits, cudaStream_t s) {
+  using C = Cfg<Kind, Mode>;
+  constexpr auto kern = grouped_bf16_kernel<Kind, Mode>;
+  cudaError_t e = prepare_kernel<kern>(C::kSmemBytes, 0);
   if (e != cudaSuccess) return e;
   Args a{};
   a.M = p.M;
@@ -449,6 +524,7 @@ cudaError_t launch_tiles(const GroupedProblem& p, cudaStream_t s) {
   a.cols = p.K;
   a.n_tiles = (p.K + C::kNTile - 1) / C::kNTile;
   a.red = Kind == kGroupedFwd ? p.K : p.N;
+  a.splits = splits;
   a.offsets = p.offsets;
   a.out = p.out;
   a.ldo = p.ldo;
@@ -480,21 +556,31 @@ cudaError_t launch_tiles(const GroupedProblem& p, cudaStream_t s) {
     tiles = (static_cast<long long>(p.M) / C::kNTile + (p.M < p.G ? p.M : p.G)) * a.m_tiles;
   }
   if (!ok) return cudaErrorInvalidValue;
-  if constexpr (kPair) {
-    return launch_pairs<kern>(tiles, C::kSmemBytes, s, tm_a, tm_b, tm_out, a);
-  } else {
+  if constexpr (Mode == kModeSingle) {
     const unsigned grid = static_cast<unsigned>(tiles < p.num_sms ? tiles : p.num_sms);
-    return launch_pdl(kern, dim3(grid), dim3(kGroupedThreads), C::kSmemBytes, s, tm_a, tm_b, tm_out, a);
+    return launch_pdl(kern, dim3(grid), dim3(kThreads), C::kSmemBytes, s, tm_a, tm_b, tm_out, a);
+  } else {
+    return launch_clusters<kern>(kThreads, splits, tiles, Mode == kModePair, C::kSmemBytes, s, tm_a, tm_b, tm_out, a);
   }
 }
 
 template <int Kind>
 cudaError_t dispatch(const GroupedProblem& p, cudaStream_t s) {
   const long long m = Kind == kGroupedDx ? p.K : p.N;
-  const long long tiles = Kind == kGroupedDw
-                              ? static_cast<long long>(p.G) * ((m + 255) / 256) * ((p.K + 255) / 256)
-                              : (static_cast<long long>(p.M) / 256 + (p.M < p.G ? p.M : p.G)) * ((m + 255) / 256);
-  return tiles >= p.num_sms / 2 ? launch_tiles<Kind, true>(p, s) : launch_tiles<Kind, false>(p, s);
+  auto tiles = [&](int tile) {
+    const long long m_tiles = (m + tile - 1) / tile;
+    return Kind == kGroupedDw ? p.G * m_tiles * ((p.K + tile - 1) / tile) : row_tiles(p.M, p.G, tile) * m_tiles;
+  };
+  const long long red = Kind == kGroupedFwd ? p.K : (Kind == kGroupedDx ? p.N : p.M / p.G);
+  const int splits = choose_splits(tiles(128), p.num_sms, static_cast<int>((red + 63) / 64));
+  if (splits > 1) return launch_tiles<Kind, kModeSplit>(p, splits, s);
+  // a stage takes a pair about as long for its 256 x 256 tile as a CTA for its 128 x 128, so the pairs win where
+  // the larger tiles do not need more rounds over the SMs
+  const long long single_rounds = (tiles(128) + p.num_sms - 1) / p.num_sms;
+  const long long pair_rounds = (tiles(256) + p.num_sms / 2 - 1) / (p.num_sms / 2);
+  return pair_rounds < single_rounds || (pair_rounds == single_rounds && pair_rounds > 1)
+             ? launch_tiles<Kind, kModePair>(p, 2, s)
+             : launch_tiles<Kind, kModeSingle>(p, 1, s);
 }
 
 }  // namespace
@@ -551,6 +637,12 @@ bool make_row_maps(RowMaps* maps, const void* base, long long rows, long long co
   for (int i = 0; i < 5; ++i)
     if (!make_grouped_map(&maps->map[i], base, 0, rows, cols, ld, elem_bytes, row_map_rows(i))) return false;
   return true;
+}
+
+int choose_splits(long long tiles, int sms, int stages) {
+  int splits = 1;
+  while (splits < 8 && tiles * splits * 2 <= sms && stages >= 4 * splits * 2) splits *= 2;
+  return splits;
 }
 
 cudaError_t launch_grouped(const GroupedProblem& p, cudaStream_t stream) {

@@ -9,27 +9,32 @@
 
 namespace moe {
 
-constexpr int kGroupedThreads = 320;  // TMA producer warp, MMA warp, two groups of four epilogue warps
-constexpr int kGroupedEpiWarps = 8;
+constexpr int kGroupedEpiWarps = 8;  // two groups of four, besides the TMA producer and the MMA issuer
 constexpr int kMaxGroups = 1024;
 constexpr int kGroupTableBytes = 2 * (kMaxGroups + 4) * 4;
 constexpr int kGroupedReserve = 1024 + kGroupTableBytes;  // barriers, then the group tables
 constexpr int kSmemMax = 232448;                          // dynamic shared memory of a block on sm_100
 
+// How a tile is computed: by one CTA, by a pair of CTAs (cta_group::2), or by a cluster that shares its reduction.
+enum GroupedMode { kModeSingle = 0, kModePair = 1, kModeSplit = 2 };
+
+// floats between two rows of a split tile's partial sums: 16-byte stores of a warp's rows spread over all banks
+constexpr int kPartialPitch = 132;
+
 // wait-site codes reported in the status word (low byte)
 constexpr int kWhereGroupedProducer = 0x41, kWhereGroupedMma = 0x42, kWhereGroupedEpilogue = 0x43,
               kWhereGroupedDrain = 0x44;
 
-// Bounded wait: polls the barrier, looking at the abort flag and the clock
-// only now and then (reading the clock costs more than a poll).
+// Bounded wait: polls the barrier, looking at the abort flag and the clock every 256 polls only.
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort, int* status, int where) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  for (int i = 1;; ++i) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 1;; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 31) == 0) {
+    if ((i & 255) == 0) {
       if (*abort) return false;
-      if (globaltimer_ns() - t0 > kWaitTimeoutNs) {
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > kWaitTimeoutNs) {
         *abort = 1;
         report_status(status, MOE_STATUS_WAIT_TIMEOUT | where);
         return false;
@@ -88,12 +93,12 @@ __device__ __forceinline__ uint32_t in_cta(const void* p, uint32_t rank) {
   return out;
 }
 
-// Arrive on a barrier of either CTA.  The arrivals hand over TMEM columns that have been read into registers
-// (ordered by the tcgen05 fences) or shared memory that the async proxy reads, no generic writes: the default
-// CTA-scope release is enough, where a cluster-scope one would wait for the thread's memory traffic each time
-// (measured: it doubled the FP8 products' time per K block).
+// Arrive on a barrier of either CTA without ordering the thread's other memory accesses.  The arrivals hand over
+// TMEM columns that are in registers by then (tcgen05.wait::ld) or shared memory that the async proxy wrote and
+// reads, no generic writes.  A cluster-scope release here waits for the thread's memory traffic each time: the FP8
+// product of 8192 x 4096 x 7168 took 531 us with it and 318 us without.
 __device__ __forceinline__ void arrive_in_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // the same behind generic writes to shared memory (made visible to the async proxy before)
@@ -236,9 +241,70 @@ __device__ __forceinline__ void stage_row(uint8_t* box, int lane, const uint4 (&
   for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(box + lane * 128 + ((c ^ (lane & 7)) << 4)) = piece[c];
 }
 
+// Values that an asynchronous TMEM load delivers may be used from here on: placed behind tcgen05.wait::ld, it keeps the
+// compiler from moving their uses in front of the wait.
+__device__ __forceinline__ void pin16(uint32_t (&v)[16]) {
+#pragma unroll
+  for (int i = 0; i < 16; i += 8)
+    asm volatile("" : "+r"(v[i]), "+r"(v[i + 1]), "+r"(v[i + 2]), "+r"(v[i + 3]), "+r"(v[i + 4]), "+r"(v[i + 5]),
+                 "+r"(v[i + 6]), "+r"(v[i + 7]));
+}
+__device__ __forceinline__ void pin32(uint32_t (&v)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 8)
+    asm volatile("" : "+r"(v[i]), "+r"(v[i + 1]), "+r"(v[i + 2]), "+r"(v[i + 3]), "+r"(v[i + 4]), "+r"(v[i + 5]),
+                 "+r"(v[i + 6]), "+r"(v[i + 7]));
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ uint4 pack_bf16x8(const float* f) {
+  return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+}
+
+__device__ __forceinline__ float4 load_in_cluster(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+// The sum of a split tile: every CTA of the cluster has its partial sums [rows][kPartialPitch] at `smem`; CTA `cta`
+// adds its part of the elements up in rank order (so the result does not depend on timing) and stores them at
+// out[at + row * ldo + column], cols a multiple of 8.
+template <int kThreads>
+__device__ __forceinline__ void add_partials(const uint8_t* smem, int cta, int splits, int rows, int cols, void* out,
+                                             long long at, long long ldo, bool out_f32, bool accumulate) {
+  const int quads = cols / 4;
+  for (int i = cta * kThreads + threadIdx.x; i < rows * quads; i += splits * kThreads) {
+    const int r = i / quads, c = (i - r * quads) * 4;
+    const uint8_t* mine = smem + (r * kPartialPitch + c) * 4;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s = 0; s < splits; ++s) {
+      const float4 p = load_in_cluster(in_cta(mine, s));
+      v.x += p.x;
+      v.y += p.y;
+      v.z += p.z;
+      v.w += p.w;
+    }
+    const long long o = at + r * ldo + c;
+    if (out_f32) {
+      float4* dst = reinterpret_cast<float4*>(static_cast<float*>(out) + o);
+      if (accumulate) {
+        const float4 b = *dst;
+        v = make_float4(b.x + v.x, b.y + v.y, b.z + v.z, b.w + v.w);
+      }
+      *dst = v;
+    } else {
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out) + o) =
+          make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+    }
+  }
 }
 
 // Descriptor of an MN-major operand written by TMA with the 128-byte swizzle
@@ -261,9 +327,10 @@ __device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t smem_addr) {
 // each group, where a group has ceil(rows / row_tile) * per_row_tile tiles.
 // Returns their number.  All threads of the block take part; ends with a
 // block barrier.
+template <int kThreads>
 __device__ __forceinline__ int build_group_tables(const int32_t* offsets, int M, int G, int row_tile, int per_row_tile,
                                                   int* off, int* first, int* scan) {
-  for (int i = threadIdx.x; i <= G; i += kGroupedThreads) {
+  for (int i = threadIdx.x; i <= G; i += kThreads) {
     const int v = offsets ? offsets[i] : (i ? M : 0);
     off[i] = v < 0 ? 0 : (v > M ? M : v);
   }
@@ -287,7 +354,7 @@ __device__ __forceinline__ int build_group_tables(const int32_t* offsets, int M,
   if (lane == 31) scan[warp] = incl;
   __syncthreads();
   int base = incl - sum, total = 0;
-  for (int w = 0; w < kGroupedThreads / 32; ++w) {
+  for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) base += scan[w];
     total += scan[w];
   }
@@ -338,50 +405,73 @@ __host__ __device__ constexpr int row_map_index(int rows) {  // the smallest box
 __host__ __device__ constexpr int row_map_rows(int index) { return index == 0 ? 16 : 32 * index; }
 bool make_row_maps(RowMaps* maps, const void* base, long long rows, long long cols, long long ld, int elem_bytes);
 
-// The dynamic shared memory limit is a property of a kernel on each device.
+// Once per kernel and device: allow its dynamic shared memory, and check that it is launched with at least `regs`
+// registers per thread.
 template <auto kKernel>
-cudaError_t allow_smem(size_t bytes) {
+cudaError_t prepare_kernel(size_t smem, int regs) {
   static bool done[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev < 64 && done[dev]) return cudaSuccess;
-  e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
-  if (e == cudaSuccess && dev < 64) done[dev] = true;
+  if (dev >= 64) return cudaErrorInvalidDevice;
+  if (done[dev]) return cudaSuccess;
+  cudaFuncAttributes attr;
+  if ((e = cudaFuncGetAttributes(&attr, kKernel)) != cudaSuccess) return e;
+  if (attr.numRegs < regs) return cudaErrorInvalidKernelImage;
+  e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e == cudaSuccess) done[dev] = true;
   return e;
 }
 
-// Launch with programmatic stream serialisation (see launch_pdl) as clusters of two CTAs; `pairs` clusters at most.
+// Launch clusters of `size` CTAs with programmatic stream serialisation (see launch_pdl).  persistent: no more than
+// are resident at once (the SMs of a GPC need not divide evenly), always of the same size.
 template <auto kKernel, typename... Args>
-cudaError_t launch_pairs(long long pairs, size_t smem, cudaStream_t stream, const Args&... args) {
-  static int fit[64] = {};  // clusters that are resident at once (the SMs of a GPC need not pair up evenly)
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev >= 64) return cudaErrorInvalidDevice;
+cudaError_t launch_clusters(int threads, int size, long long clusters, bool persistent, size_t smem,
+                            cudaStream_t stream, const Args&... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kGroupedThreads);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(size);
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  if (fit[dev] == 0) {
-    cfg.numAttrs = 1;
-    cfg.gridDim = dim3(2);
-    int n = 0;
-    e = cudaOccupancyMaxActiveClusters(&n, kKernel, &cfg);
+  if (persistent) {
+    static int fit[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    fit[dev] = n > 0 ? n : 1;
+    if (dev >= 64) return cudaErrorInvalidDevice;
+    if (fit[dev] == 0) {
+      cfg.numAttrs = 1;
+      cfg.gridDim = dim3(static_cast<unsigned>(size));
+      int n = 0;
+      e = cudaOccupancyMaxActiveClusters(&n, kKernel, &cfg);
+      if (e != cudaSuccess) return e;
+      fit[dev] = n > 0 ? n : 1;
+    }
+    if (clusters > fit[dev]) clusters = fit[dev];
   }
   cfg.numAttrs = 2;
-  cfg.gridDim = dim3(static_cast<unsigned>(2 * (pairs < fit[dev] ? pairs : fit[dev])));
+  cfg.gridDim = dim3(static_cast<unsigned>(clusters * size));
   return cudaLaunchKernelEx(&cfg, kKernel, args...);
 }
+
+// Row tiles of `tile` rows that M rows in G groups come to: exact for one group, otherwise an estimate (the host does
+// not see the offsets): every group that can have rows ends in half a tile.
+inline long long row_tiles(long long M, long long G, int tile) {
+  const long long groups = M < G ? M : G;
+  if (G == 1) return (M + tile - 1) / tile;
+  const long long n = M / tile + (groups + 1) / 2;
+  return n > groups ? n : groups;
+}
+
+// CTAs that share a tile's reduction: as many (1, 2, 4, 8) as leave each at least four stages and do not make more
+// CTAs than SMs.
+int choose_splits(long long tiles, int sms, int stages);
 
 }  // namespace moe

@@ -22,7 +22,6 @@ namespace moe {
 namespace {
 
 constexpr int kMaxRowThreads = 1024;
-constexpr int kMaxBackwardBlocks = 296;  // two per SM; fixed, so that the workspace does not depend on the device
 
 struct alignas(16) bf16x8 {
   __nv_bfloat162 h[4];
@@ -66,26 +65,40 @@ __device__ __forceinline__ float block_sum(float v, int warps, float* buf) {
 }
 
 // Scale and E4M3 codes of the 128-column group that this thread's half-warp
-// holds, 8 columns each (columns past the row's end are zeros).  The scale
-// is that of the finite values; a value that is not finite becomes the NaN
-// code (E4M3 has no infinity, and saturating would hide it).
-__device__ __forceinline__ uint2 quantize8(const float (&f)[8], float* scale_out) {
-  float amax = 0.f;
+// holds, 8 bf16 columns each (columns past the row's end are zeros).  Without
+// their signs bf16 numbers compare as integers, infinity and NaN above the
+// rest, so the largest is found two at a time without conversions; only a
+// group whose largest is not finite looks again: the scale is that of the
+// finite values, and a value that is not finite becomes the NaN code (E4M3 has
+// no infinity, and saturating would hide it).
+__device__ __forceinline__ uint2 quantize8(const uint4& u, float* scale_out) {
+  constexpr uint32_t kAbs = 0x7fff7fffu, kInf = 0x7f80u;
+  uint32_t m = __vmaxu2(__vmaxu2(u.x & kAbs, u.y & kAbs), __vmaxu2(u.z & kAbs, u.w & kAbs));
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float a = fabsf(f[i]);
-    amax = fmaxf(amax, a <= 3.402823466e38f ? a : 0.f);  // false for NaN and infinity
+  for (int o = 8; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+  uint32_t top = max(m & 0xffffu, m >> 16);
+  const bool odd = top >= kInf;  // the same on all lanes of the half-warp
+  float f[8];
+  unpack8(u, f);
+  if (__any_sync(0xffffffffu, odd)) {
+    uint32_t finite = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t b = (__float_as_uint(f[i]) >> 16) & 0x7fffu;
+      if (b < kInf) finite = max(finite, b);
+      else f[i] = __int_as_float(0x7fc00000);
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) finite = max(finite, __shfl_xor_sync(0xffffffffu, finite, o));
+    top = finite;
   }
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  const float scale = act_scale_from_amax(amax);
+  const float scale = act_scale_from_amax(__uint_as_float(top << 16));
   const float inv = pow2_recip(scale);
-  float q[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) q[i] = fabsf(f[i]) <= 3.402823466e38f ? f[i] * inv : __int_as_float(0x7fc00000);
   uint2 c;
-  c.x = static_cast<uint32_t>(f32x2_to_e4m3x2(q[0], q[1])) | (static_cast<uint32_t>(f32x2_to_e4m3x2(q[2], q[3])) << 16);
-  c.y = static_cast<uint32_t>(f32x2_to_e4m3x2(q[4], q[5])) | (static_cast<uint32_t>(f32x2_to_e4m3x2(q[6], q[7])) << 16);
+  c.x = static_cast<uint32_t>(f32x2_to_e4m3x2(f[0] * inv, f[1] * inv)) |
+        (static_cast<uint32_t>(f32x2_to_e4m3x2(f[2] * inv, f[3] * inv)) << 16);
+  c.y = static_cast<uint32_t>(f32x2_to_e4m3x2(f[4] * inv, f[5] * inv)) |
+        (static_cast<uint32_t>(f32x2_to_e4m3x2(f[6] * inv, f[7] * inv)) << 16);
   *scale_out = scale;
   return c;
 }
@@ -93,9 +106,11 @@ __device__ __forceinline__ uint2 quantize8(const float (&f)[8], float* scale_out
 // ----------------------------------------------------------------------------
 // forward: blockDim.x threads per row (a multiple of 32), V vectors of 8
 // columns each; blockDim.y rows per block when one warp covers a row.
+// (V = 4 is held to 64 registers: with the 85 that it would take, half as many
+// rows are in flight and 8192 x 7168 takes 100 us instead of 73.)
 // ----------------------------------------------------------------------------
 template <int V>
-__global__ void __launch_bounds__(kMaxRowThreads) rms_norm_kernel(const RmsNormArgs a) {
+__global__ void __launch_bounds__(V == 4 ? kMaxNormH / 32 : kMaxRowThreads, V == 4 ? 2 : 1) rms_norm_kernel(const RmsNormArgs a) {
   pdl_launch_dependents();
   pdl_wait();
   __shared__ float sums[32];
@@ -161,9 +176,8 @@ __global__ void __launch_bounds__(kMaxRowThreads) rms_norm_kernel(const RmsNormA
     const uint4 y = pack8(f);
     if (a.y && v < vecs) *reinterpret_cast<uint4*>(a.y + row * a.ldy + 8 * v) = y;
     if (a.codes) {
-      unpack8(y, f);
       float scale;
-      const uint2 c = quantize8(f, &scale);
+      const uint2 c = quantize8(y, &scale);
       if (v < vecs) {
         *reinterpret_cast<uint2*>(a.codes + row * a.H + 8 * v) = c;
         if ((v & 15) == 0) a.scales[static_cast<long long>(v >> 4) * a.T + row] = scale;
@@ -176,14 +190,21 @@ __global__ void __launch_bounds__(kMaxRowThreads) rms_norm_kernel(const RmsNormA
 // backward: a block walks rows (grid stride) and keeps its columns' weight
 // gradient in registers; each block writes one row of partial sums, which the
 // second kernel adds in block order, so the result does not depend on timing.
+// The next row's loads are in flight while a row's sum is formed.  Up to 512
+// columns a warp holds a row by itself and 16 of them share a block (then the
+// block adds their columns through shared memory first); otherwise the whole
+// block holds one row.
 // ----------------------------------------------------------------------------
 template <int V, bool kRes>
 __global__ void __launch_bounds__(kMaxRowThreads) rms_norm_backward_kernel(const RmsNormBackwardArgs a) {
   pdl_launch_dependents();
   pdl_wait();
   __shared__ float sums[2][32];
+  extern __shared__ float columns[];  // blockDim.y > 1: [blockDim.y][H]
   const int vecs = a.H / 8;
   const int warps = blockDim.x >> 5;
+  const long long first_row = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
+  const long long step = static_cast<long long>(gridDim.x) * blockDim.y;
   float acc[V][8];
   uint4 w[V];
 #pragma unroll
@@ -209,9 +230,13 @@ __global__ void __launch_bounds__(kMaxRowThreads) rms_norm_backward_kernel(const
   };
   const float inv_h = 1.0f / static_cast<float>(a.H);
   int buf = 0;
-  for (long long row = blockIdx.x; row < a.T; row += gridDim.x) {
-    load(row);
-    const float rstd = a.rstd[row];
+  float next_rstd = 0.f;
+  if (first_row < a.T) {
+    load(first_row);
+    next_rstd = a.rstd[first_row];
+  }
+  for (long long row = first_row; row < a.T; row += step) {
+    const float rstd = next_rstd;
     float dot = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -226,16 +251,28 @@ __global__ void __launch_bounds__(kMaxRowThreads) rms_norm_backward_kernel(const
         dot = fmaf(df[j] * wf[j], n, dot);
       }
     }
+    // the next row is under way while this one's sum is formed
+    uint4 cd[V], cs[V], cr[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      cd[i] = d[i];
+      cs[i] = s[i];
+      cr[i] = r[i];
+    }
+    if (row + step < a.T) {
+      load(row + step);
+      next_rstd = a.rstd[row + step];
+    }
     const float c = block_sum(dot, warps, sums[buf]) * inv_h;
     buf ^= 1;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int v = i * blockDim.x + threadIdx.x;
       float df[8], sf[8], wf[8], rf[8];
-      unpack8(d[i], df);
-      unpack8(s[i], sf);
+      unpack8(cd[i], df);
+      unpack8(cs[i], sf);
       unpack8(w[i], wf);
-      unpack8(r[i], rf);
+      unpack8(cr[i], rf);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float n = sf[j] * rstd;
@@ -246,6 +283,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) rms_norm_backward_kernel(const
     }
   }
   float* part = a.partials + static_cast<long long>(blockIdx.x) * a.H;
+  if (blockDim.y > 1) part = columns + threadIdx.y * a.H;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int v = i * blockDim.x + threadIdx.x;
@@ -253,6 +291,15 @@ __global__ void __launch_bounds__(kMaxRowThreads) rms_norm_backward_kernel(const
       float4* p = reinterpret_cast<float4*>(part + 8 * v);
       p[0] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
       p[1] = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
+    }
+  }
+  if (blockDim.y > 1) {
+    __syncthreads();
+    const int threads = blockDim.x * blockDim.y;
+    for (int h = threadIdx.y * blockDim.x + threadIdx.x; h < a.H; h += threads) {
+      float v = 0.f;
+      for (int y = 0; y < static_cast<int>(blockDim.y); ++y) v += columns[y * a.H + h];
+      a.partials[static_cast<long long>(blockIdx.x) * a.H + h] = v;
     }
   }
 }
@@ -276,26 +323,39 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float* partials,
 // ----------------------------------------------------------------------------
 // the row format by itself: a half-warp quantises one 128-column group
 // ----------------------------------------------------------------------------
+template <int kItems>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const __nv_bfloat16* x, long long ldx, long long rows,
-                                                            int cols, uint8_t* codes, float* scales) {
+                                                            int cols, int block_rows, uint8_t* codes, float* scales) {
   pdl_launch_dependents();
   pdl_wait();
+  // a block takes kItems * 16 groups of `block_rows` rows, or of a part of one row (block_rows = 1)
   const int groups = (cols + 127) / 128;
-  const long long items = rows * groups;
-  const long long item = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 4;
-  const bool in = item < items;  // uniform over a half-warp; all lanes take part in the shuffles
-  const long long row = in ? item / groups : 0;
-  const int g = in ? static_cast<int>(item - row * groups) : 0;
-  const int col = g * 128 + (threadIdx.x & 15) * 8;
-  const bool live = in && col < cols;
-  uint4 u = make_uint4(0, 0, 0, 0);
-  if (live) u = ld16(x + row * ldx + col);
-  float f[8];
-  unpack8(u, f);
-  float scale;
-  const uint2 c = quantize8(f, &scale);
-  if (live) *reinterpret_cast<uint2*>(codes + row * cols + col) = c;
-  if (in && (threadIdx.x & 15) == 0) scales[static_cast<long long>(g) * rows + row] = scale;
+  const int parts = (groups + kItems * 16 - 1) / (kItems * 16);  // blocks of a row
+  const long long row0 = block_rows > 1 ? static_cast<long long>(blockIdx.x) * block_rows : blockIdx.x / parts;
+  const int group0 = block_rows > 1 ? 0 : static_cast<int>(blockIdx.x % parts) * kItems * 16;
+  const int half = threadIdx.x >> 4, l = threadIdx.x & 15;
+  long long row[kItems];
+  int g[kItems];
+  bool in[kItems];
+  uint4 u[kItems];
+#pragma unroll
+  for (int i = 0; i < kItems; ++i) {
+    const int item = i * 16 + half;
+    const int r = block_rows > 1 ? item / groups : 0;
+    row[i] = row0 + r;
+    g[i] = group0 + item - r * groups;
+    in[i] = (block_rows == 1 || r < block_rows) && row[i] < rows && g[i] < groups;  // uniform over a half-warp
+    u[i] = make_uint4(0, 0, 0, 0);
+    if (in[i] && g[i] * 128 + 8 * l < cols) u[i] = ld16(x + row[i] * ldx + g[i] * 128 + 8 * l);
+  }
+#pragma unroll
+  for (int i = 0; i < kItems; ++i) {
+    float scale;
+    const uint2 c = quantize8(u[i], &scale);  // all lanes take part in the shuffles
+    const int col = g[i] * 128 + 8 * l;
+    if (in[i] && col < cols) *reinterpret_cast<uint2*>(codes + row[i] * cols + col) = c;
+    if (in[i] && l == 0) scales[static_cast<long long>(g[i]) * rows + row[i]] = scale;
+  }
 }
 
 // 16 codes per thread; the scale is a power of two, so bf16 holds the value exactly (subnormals of
@@ -308,7 +368,9 @@ __global__ void __launch_bounds__(256) dequantize_rows_kernel(const uint8_t* cod
   const int per_row = cols / 16;
   const long long item = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
   if (item >= rows * per_row) return;
-  const long long row = item / per_row;
+  // (a 64-bit division takes longer than the rest of the thread's work)
+  const long long row = item < (1ll << 32) ? static_cast<uint32_t>(item) / static_cast<uint32_t>(per_row)
+                                           : item / per_row;
   const int col = static_cast<int>(item - row * per_row) * 16;
   const uint4 u = *reinterpret_cast<const uint4*>(codes + row * cols + col);
   const float s = scales[static_cast<long long>(col >> 7) * rows + row];
@@ -341,28 +403,56 @@ int row_threads(int vecs, int v) { return ((vecs + v - 1) / v + 31) / 32 * 32; }
 
 cudaError_t launch_rms_norm(const RmsNormArgs& a, cudaStream_t stream) {
   const int vecs = a.H / 8;
-  const int v = vecs > 1024 ? 2 : 1;
+  // Few rows: a thread per vector, the shortest way through one row.  Many: up to four vectors per thread, so that
+  // an SM has more rows in flight (T = 8192, H = 7168, residual and FP8 output: 101 us with one, 73 us with four).
+  const int v = a.T <= 2 * 148 ? (vecs > 1024 ? 2 : 1) : (vecs > 64 ? 4 : (vecs > 32 ? 2 : 1));
   const int tx = row_threads(vecs, v);
   const int ty = tx == 32 ? 8 : 1;
   const dim3 block(tx, ty);
-  const unsigned grid = static_cast<unsigned>((static_cast<long long>(a.T) + ty - 1) / ty);
-  if (v == 1) return launch_pdl(rms_norm_kernel<1>, dim3(grid), block, 0, stream, a);
-  return launch_pdl(rms_norm_kernel<2>, dim3(grid), block, 0, stream, a);
+  const dim3 grid(static_cast<unsigned>((static_cast<long long>(a.T) + ty - 1) / ty));
+  if (v == 1) return launch_pdl(rms_norm_kernel<1>, grid, block, 0, stream, a);
+  if (v == 2) return launch_pdl(rms_norm_kernel<2>, grid, block, 0, stream, a);
+  return launch_pdl(rms_norm_kernel<4>, grid, block, 0, stream, a);
 }
 
-int rms_norm_backward_blocks(int T) { return T < kMaxBackwardBlocks ? T : kMaxBackwardBlocks; }
+namespace {
+
+// the backward kernel's block: threads per row, rows at a time, vectors per thread
+struct BackwardShape {
+  int tx, ty, v;
+};
+
+BackwardShape backward_shape(int H) {
+  const int vecs = H / 8;
+  if (vecs <= 64) return {32, 16, vecs > 32 ? 2 : 1};
+  const int v = vecs > 1024 ? 2 : 1;
+  return {row_threads(vecs, v), 1, v};
+}
+
+template <bool kRes>
+cudaError_t launch_backward_rows(const RmsNormBackwardArgs& a, int blocks, cudaStream_t stream) {
+  const BackwardShape b = backward_shape(a.H);
+  const size_t smem = b.ty > 1 ? static_cast<size_t>(b.ty) * a.H * sizeof(float) : 0;  // at most 32 KB
+  if (b.v == 1)
+    return launch_pdl(rms_norm_backward_kernel<1, kRes>, dim3(blocks), dim3(b.tx, b.ty), smem, stream, a);
+  return launch_pdl(rms_norm_backward_kernel<2, kRes>, dim3(blocks), dim3(b.tx, b.ty), smem, stream, a);
+}
+
+}  // namespace
+
+// Enough blocks for about 1024 threads per SM; fixed numbers, so that neither the workspace nor the order of the
+// sums depends on the device.
+int rms_norm_backward_blocks(int T, int H) {
+  const BackwardShape b = backward_shape(H);
+  const int threads = b.tx * b.ty;
+  const int most = threads >= 512 ? 2 * 148 : 148 * (1024 / threads > 8 ? 8 : 1024 / threads);
+  const int want = (T + b.ty - 1) / b.ty;
+  return want < most ? want : most;
+}
 
 cudaError_t launch_rms_norm_backward(const RmsNormBackwardArgs& a, float* dweight, int blocks, cudaStream_t stream) {
-  const int vecs = a.H / 8;
-  const int v = vecs > 1024 ? 2 : 1;
-  const int tx = row_threads(vecs, v);
-  cudaError_t e;
-  if (a.dresidual)
-    e = v == 1 ? launch_pdl(rms_norm_backward_kernel<1, true>, dim3(blocks), dim3(tx), 0, stream, a)
-               : launch_pdl(rms_norm_backward_kernel<2, true>, dim3(blocks), dim3(tx), 0, stream, a);
-  else
-    e = v == 1 ? launch_pdl(rms_norm_backward_kernel<1, false>, dim3(blocks), dim3(tx), 0, stream, a)
-               : launch_pdl(rms_norm_backward_kernel<2, false>, dim3(blocks), dim3(tx), 0, stream, a);
+  const cudaError_t e =
+      a.dresidual ? launch_backward_rows<true>(a, blocks, stream) : launch_backward_rows<false>(a, blocks, stream);
   if (e != cudaSuccess) return e;
   return launch_pdl(column_sum_kernel, dim3((a.H + 31) / 32), dim3(32, 32), 0, stream,
                     static_cast<const float*>(a.partials), blocks, a.H, dweight);
@@ -370,9 +460,20 @@ cudaError_t launch_rms_norm_backward(const RmsNormBackwardArgs& a, float* dweigh
 
 cudaError_t launch_quantize_rows(const void* x, long long ldx, long long rows, int cols, uint8_t* codes,
                                  float* scales, cudaStream_t stream) {
-  const long long threads = rows * ((cols + 127) / 128) * 16;
-  return launch_pdl(quantize_rows_kernel, dim3(static_cast<unsigned>((threads + 255) / 256)), dim3(256), 0, stream,
-                    static_cast<const __nv_bfloat16*>(x), ldx, rows, cols, codes, scales);
+  const int groups = (cols + 127) / 128;
+  // four groups per half-warp where there is work for every SM (8192 x 7168: 52 us with one, 45 us with four)
+  const int items = rows * groups >= 148 * 8 * 64 ? 4 : 1;
+  const int block_rows = groups < items * 16 ? items * 16 / groups : 1;
+  const long long blocks = block_rows > 1 ? (rows + block_rows - 1) / block_rows
+                                          : rows * ((groups + items * 16 - 1) / (items * 16));
+  if (blocks >= (1ll << 31)) return cudaErrorInvalidConfiguration;
+  const dim3 grid(static_cast<unsigned>(blocks));
+  const __nv_bfloat16* xb = static_cast<const __nv_bfloat16*>(x);
+  if (items == 4)
+    return launch_pdl(quantize_rows_kernel<4>, grid, dim3(256), 0, stream, xb, ldx, rows, cols, block_rows, codes,
+                      scales);
+  return launch_pdl(quantize_rows_kernel<1>, grid, dim3(256), 0, stream, xb, ldx, rows, cols, block_rows, codes,
+                    scales);
 }
 
 cudaError_t launch_dequantize_rows(const uint8_t* codes, const float* scales, long long rows, int cols, void* x,

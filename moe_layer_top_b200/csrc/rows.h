@@ -44,7 +44,7 @@ constexpr int kMaxNormH = 16384;
 cudaError_t launch_rms_norm(const RmsNormArgs& a, cudaStream_t stream);
 
 // blocks of the backward kernel (each leaves one row of weight-gradient partial sums)
-int rms_norm_backward_blocks(int T);
+int rms_norm_backward_blocks(int T, int H);
 cudaError_t launch_rms_norm_backward(const RmsNormBackwardArgs& a, float* dweight, int blocks, cudaStream_t stream);
 
 cudaError_t launch_quantize_rows(const void* x, long long ldx, long long rows, int cols, uint8_t* codes,

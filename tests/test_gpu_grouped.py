@@ -40,6 +40,8 @@ SIZES = [
     [7] * 20, [64, 1, 64, 200, 33, 0, 0, 5],
 ]
 # enough tiles for the kernels that pair two SMs
+# and few tiles with long reductions for those that share one
+LONG = [([3], 136, 2048), ([40, 0, 2], 264, 1104), ([130], 128, 4096)]
 LARGE = [([700, 0, 300, 33, 513, 1000], 2056, 528), ([1, 2048, 31, 257, 256, 255], 2304, 464)]
 SHAPES = [(8, 8), (64, 64), (128, 128), (136, 72), (256, 1024), (264, 328), (1000, 200), (56, 520)]
 
@@ -50,7 +52,7 @@ def _cases():
     for i, sizes in enumerate(SIZES):
         for j in (i, i + 3):
             out.append((sizes, *SHAPES[j % len(SHAPES)]))
-    return out + LARGE + [(sizes, K, N) for sizes, N, K in LARGE]
+    return out + LARGE + LONG + [(sizes, K, N) for sizes, N, K in LARGE + LONG] + [([2000], 136, 72), ([700, 900], 264, 56)]
 
 
 def _forward(x, w, off, N, M, **kw):
