@@ -126,8 +126,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const __grid_constant__ CUtensorMap tm_out, const Args args) {
   using C = Cfg<Kind, Mode>;
   constexpr bool kPair = C::kPair, kSplit = Mode == kModeSplit;
-  // dw in a pair: each CTA counts its own copies, clears its own tail and tells the leader
-  constexpr bool kRelay = kPair && Kind == kGroupedDw;
+  // dw in a pair: a stage in which the group ends is counted, and cleared, by each CTA for itself, and the peer
+  // tells the leader when its half is ready (for every stage that would cost 28 of 258 us at 8192 x 4096 x 4096)
+  constexpr bool kTails = kPair && Kind == kGroupedDw;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* staging = smem + static_cast<size_t>(C::kStages) * C::kStageBytes;
@@ -135,7 +136,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(reserve);
   uint64_t* empty = full + C::kStages;
   uint64_t* peer_full = empty + C::kStages;
-  uint64_t* acc_full = peer_full + C::kStages;
+  uint64_t* tail_full = peer_full + C::kStages;
+  uint64_t* acc_full = tail_full + C::kStages;
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* drain = acc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -143,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* scan = reinterpret_cast<int*>(reserve + 640);
   int* off = reinterpret_cast<int*>(reserve + 1024);
   int* first = off + kMaxGroups + 4;
-  static_assert((3 * C::kStages + 5) * 8 + 8 <= 640, "barriers overlap the scan buffer");
+  static_assert((4 * C::kStages + 5) * 8 + 8 <= 640, "barriers overlap the scan buffer");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cta = kPair || kSplit ? static_cast<int>(cluster_rank()) : 0;  // rank in the cluster
@@ -155,6 +157,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
       mbar_init(&peer_full[s], 1);
+      mbar_init(&tail_full[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
@@ -207,40 +210,43 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           uint8_t* a = smem + static_cast<size_t>(stage) * C::kStageBytes;
           uint8_t* b = a + C::kABytes;
-          constexpr bool kLead = kPair && !kRelay;  // copies of both CTAs count on the leader's barrier
           uint32_t bar = smem_u32(&full[stage]);
-          if constexpr (kLead) {
+          if (kTails && k + 64 > tl.red) {  // the group ends here: each CTA counts its own copies
+            uint64_t* own = leader ? &full[stage] : &tail_full[stage];
+            mbar_arrive_expect_tx(own, bytes);
+            bar = in_cta(own, rank);
+          } else if (kPair) {               // copies of both CTAs count on the leader's barrier
             if (leader) mbar_arrive_expect_tx(&full[stage], 2 * bytes);
             bar = in_cta(&full[stage], 0);
           } else {
             mbar_arrive_expect_tx(&full[stage], bytes);
           }
           if constexpr (Kind == kGroupedFwd) {
-            load_3d<kLead>(a, &tm_a, bar, k, m0, tl.g, pol);
+            load_3d<kPair>(a, &tm_a, bar, k, m0, tl.g, pol);
           } else if constexpr (Kind == kGroupedDx) {
             if (args.wide_a) {
-              load_4d<kLead>(a, &tm_a, bar, 0, k, m0 >> 6, tl.g, pol);
+              load_4d<kPair>(a, &tm_a, bar, 0, k, m0 >> 6, tl.g, pol);
             } else {
-              load_3d<kLead>(a, &tm_a, bar, m0, k, tl.g, pol);
-              load_3d<kLead>(a + 8192, &tm_a, bar, m0 + 64, k, tl.g, pol);
+              load_3d<kPair>(a, &tm_a, bar, m0, k, tl.g, pol);
+              load_3d<kPair>(a + 8192, &tm_a, bar, m0 + 64, k, tl.g, pol);
             }
           } else {
             if (args.wide_a) {
-              load_4d<kLead>(a, &tm_a, bar, 0, tl.red0 + k, m0 >> 6, 0, pol);
+              load_4d<kPair>(a, &tm_a, bar, 0, tl.red0 + k, m0 >> 6, 0, pol);
             } else {
-              load_3d<kLead>(a, &tm_a, bar, m0, tl.red0 + k, 0, pol);
-              load_3d<kLead>(a + 8192, &tm_a, bar, m0 + 64, tl.red0 + k, 0, pol);
+              load_3d<kPair>(a, &tm_a, bar, m0, tl.red0 + k, 0, pol);
+              load_3d<kPair>(a + 8192, &tm_a, bar, m0 + 64, tl.red0 + k, 0, pol);
             }
           }
           if constexpr (Kind == kGroupedDw) {
             if (args.wide_b) {
-              load_4d<kLead>(b, &tm_b.map[0], bar, 0, tl.red0 + k, n0 >> 6, 0, pol);
+              load_4d<kPair>(b, &tm_b.map[0], bar, 0, tl.red0 + k, n0 >> 6, 0, pol);
             } else {
-              load_3d<kLead>(b, &tm_b.map[0], bar, n0, tl.red0 + k, 0, pol);
-              load_3d<kLead>(b + 8192, &tm_b.map[0], bar, n0 + 64, tl.red0 + k, 0, pol);
+              load_3d<kPair>(b, &tm_b.map[0], bar, n0, tl.red0 + k, 0, pol);
+              load_3d<kPair>(b + 8192, &tm_b.map[0], bar, n0 + 64, tl.red0 + k, 0, pol);
             }
           } else {
-            load_2d<kLead>(b, &tm_b.map[box], bar, k, n0, pol);
+            load_2d<kPair>(b, &tm_b.map[box], bar, k, n0, pol);
           }
           ++fills;
           if (++stage == C::kStages) {
@@ -249,23 +255,39 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      // (the leader's barriers count both CTAs' copies)
-      if (!ok && (kRelay || leader)) drain_copies(full, C::kStages, fills);
+      if (!ok && leader) drain_copies(full, C::kStages, fills);  // the leader's barriers count both CTAs' copies
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issuer: the whole warp walks, lane 0 issues
     int stage = 0, abuf = 0;
     uint32_t phase = 0, aphase = 0;
+    uint32_t tails = 0;  // kTails: phase of each stage's tail barriers
     bool ok = true;
-    if (leader || kRelay) {
+    auto next_stage = [&](int n) {
+      stage += n;
+      while (stage >= C::kStages) {
+        stage -= C::kStages;
+        phase ^= 1u;
+      }
+    };
+    // the rows behind the group's end in a stage with `live` of them, cleared up to the next step of 16
+    // (the swizzle permutes 16-byte pieces inside a 128-byte row only, so whole rows are cleared)
+    auto clear_tail = [&](uint8_t* st, int live) {
+      const int dead = (live + 15) / 16 * 16 - live;
+      for (int i = lane; i < 4 * dead * 8; i += 32) {
+        const int box = i / (dead * 8), r = i / 8 % dead, c = i & 7;
+        *reinterpret_cast<uint4*>(st + box * 8192 + (live + r) * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+    };
+    if (leader) {
       for (int t = first_tile; t < num_tiles && ok; t += stride) {
         const Tile tl = tile_at<Kind, Mode>(args, off, first, t);
         const int k0 = red_begin(tl), k1 = red_end(tl);
         if (k0 >= k1) continue;
-        if (leader) {
-          ok = warp_wait_bar(&acc_empty[abuf], aphase ^ 1u, abort_flag, args.status, kWhereGroupedMma);
-          if (!ok) break;
-        }
+        ok = warp_wait_bar(&acc_empty[abuf], aphase ^ 1u, abort_flag, args.status, kWhereGroupedMma);
+        if (!ok) break;
         const uint32_t idesc = C::kIdesc | (static_cast<uint32_t>(tl.n >> 3) << 17);
         const uint32_t d = tmem_base + static_cast<uint32_t>(abuf * C::kNTile);
         for (int k = k0; k < k1; k += 64) {
@@ -273,54 +295,45 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           uint8_t* st = smem + static_cast<size_t>(stage) * C::kStageBytes;
           int steps = 4;
-          if constexpr (Kind == kGroupedDw) {
-            const int live = tl.red - k;
-            if (live < 64) {
-              // the group ends inside this stage: clear the rows behind it up to the next step of 16
-              // (the swizzle permutes 16-byte pieces inside a 128-byte row only, so whole rows are cleared)
-              steps = (live + 15) / 16;
-              const int dead = 16 * steps - live;
-              for (int i = lane; i < 4 * dead * 8; i += 32) {
-                const int box = i / (dead * 8), r = i / 8 % dead, c = i & 7;
-                *reinterpret_cast<uint4*>(st + box * 8192 + (live + r) * 128 + c * 16) = make_uint4(0, 0, 0, 0);
-              }
-              fence_proxy_async_smem();
-              __syncwarp();
-            }
-          }
-          if constexpr (kRelay) {
-            if (!leader) {
-              if (lane == 0) {
-                const uint32_t bar = in_cta(&peer_full[stage], 0);
-                if (tl.red - k < 64) arrive_in_cluster_release(bar); else arrive_in_cluster(bar);
-              }
-            } else {
-              ok = warp_wait_bar(&peer_full[stage], phase, abort_flag, args.status, kWhereGroupedMma);
+          if (Kind == kGroupedDw && k + 64 > tl.red) {
+            steps = (tl.red - k + 15) / 16;
+            clear_tail(st, tl.red - k);
+            if constexpr (kTails) {
+              ok = warp_wait_bar(&peer_full[stage], tails >> stage & 1u, abort_flag, args.status, kWhereGroupedMma);
               if (!ok) break;
+              tails ^= 1u << stage;
             }
           }
-          if (leader) {
-            tc_fence_after();
-            if (lane == 0) {
-              const uint32_t a = smem_u32(st), b = a + C::kABytes;
-              for (int s = 0; s < steps; ++s) {
-                const uint64_t ad = C::kMnA ? smem_desc_mn_sw128(a + 2048 * s) : smem_desc_sw128(a + 32 * s);
-                const uint64_t bd = C::kMnB ? smem_desc_mn_sw128(b + 2048 * s) : smem_desc_sw128(b + 32 * s);
-                mma_bf16_for<kPair>(d, ad, bd, idesc, (k > k0 || s > 0) ? 1u : 0u);
-              }
-              commit_for<kPair>(&empty[stage]);
+          tc_fence_after();
+          if (lane == 0) {
+            const uint32_t a = smem_u32(st), b = a + C::kABytes;
+            for (int s = 0; s < steps; ++s) {
+              const uint64_t ad = C::kMnA ? smem_desc_mn_sw128(a + 2048 * s) : smem_desc_sw128(a + 32 * s);
+              const uint64_t bd = C::kMnB ? smem_desc_mn_sw128(b + 2048 * s) : smem_desc_sw128(b + 32 * s);
+              mma_bf16_for<kPair>(d, ad, bd, idesc, (k > k0 || s > 0) ? 1u : 0u);
             }
-            __syncwarp();
+            commit_for<kPair>(&empty[stage]);
           }
-          if (++stage == C::kStages) {
-            stage = 0;
-            phase ^= 1u;
-          }
+          __syncwarp();
+          next_stage(1);
         }
         if (!ok) break;
-        if (leader && lane == 0) commit_for<kPair>(&acc_full[abuf]);
+        if (lane == 0) commit_for<kPair>(&acc_full[abuf]);
         abuf ^= 1;
         if (abuf == 0) aphase ^= 1u;
+      }
+    } else if constexpr (kTails) {
+      // the peer's tails: cleared here, then handed to the leader
+      for (int t = first_tile; t < num_tiles && ok; t += stride) {
+        const Tile tl = tile_at<Kind, Mode>(args, off, first, t);
+        next_stage(tl.red / 64);
+        if (tl.red % 64 == 0) continue;
+        ok = warp_wait_bar(&tail_full[stage], tails >> stage & 1u, abort_flag, args.status, kWhereGroupedMma);
+        if (!ok) break;
+        tails ^= 1u << stage;
+        clear_tail(smem + static_cast<size_t>(stage) * C::kStageBytes, tl.red % 64);
+        if (lane == 0) arrive_in_cluster_release(in_cta(&peer_full[stage], 0));
+        next_stage(1);
       }
     }
     // every MMA this thread issued has completed once `drain` flips
@@ -350,8 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
       }
       if constexpr (Kind != kGroupedDw) {
-        // a lane holds one output column of every row: a warp stores 32 consecutive columns of a row at once
-        // (64 bytes in bf16, whole sectors)
+        // a lane holds one output column of every row
         if (live) {
           const int chunks = (tl.valid + 15) / 16;
           for (int c = g; c < chunks; c += 2) {
@@ -373,18 +385,37 @@ __global__ void __launch_bounds__(kThreads, 1)
               float* p = reinterpret_cast<float*>(smem) + 16 * c * kPartialPitch + row;
 #pragma unroll
               for (int i = 0; i < 16; ++i) p[i * kPartialPitch] = v[i];
-            } else if (m < args.m_rows) {
-              const long long at = (static_cast<long long>(tl.n0) + 16 * c) * args.ldo + m;
-              if (args.out_f32) {
-                float* o = static_cast<float*>(args.out) + at;
+            } else if (args.out_f32) {
+              float* o = static_cast<float*>(args.out) + (static_cast<long long>(tl.n0) + 16 * c) * args.ldo + m;
+              if (m < args.m_rows) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                   if (i < n) o[i * args.ldo] = v[i];
-              } else {
-                __nv_bfloat16* o = static_cast<__nv_bfloat16*>(args.out) + at;
+              }
+            } else {
+              // four neighbouring lanes exchange what they have of four rows, so that each stores four columns of
+              // one: 8 bytes per lane, 64 bytes of each of four rows per instruction
+              uint32_t u[8], w[8];
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                  if (i < n) o[i * args.ldo] = __float2bfloat16_rn(v[i]);
+              for (int i = 0; i < 8; ++i) {
+                const uint32_t mine = pack_bf16(v[2 * i], v[2 * i + 1]);  // rows 2 i and 2 i + 1 of this column
+                const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
+                u[i] = lane & 1 ? __byte_perm(other, mine, 0x7632) : __byte_perm(mine, other, 0x5410);
+              }
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, lane & 2 ? u[2 * j] : u[2 * j + 1], 2);
+                w[2 * j] = lane & 2 ? got : u[2 * j];
+                w[2 * j + 1] = lane & 2 ? u[2 * j + 1] : got;
+              }
+              const int r = lane & 3;  // this lane's rows: r + 4 j
+              __nv_bfloat16* o = static_cast<__nv_bfloat16*>(args.out) +
+                                 (static_cast<long long>(tl.n0) + 16 * c + r) * args.ldo + (m & ~3);
+              if (m < args.m_rows) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  if (r + 4 * j < n)
+                    *reinterpret_cast<uint2*>(o + 4 * j * args.ldo) = make_uint2(w[2 * j], w[2 * j + 1]);
               }
             }
           }
