@@ -34,5 +34,6 @@ struct GroupedProblem {
 
 cudaError_t launch_grouped(const GroupedProblem& p, cudaStream_t stream);
 cudaError_t launch_grouped_fp8(const GroupedProblem& p, cudaStream_t stream);
+cudaError_t launch_grouped_fp8_pair(const GroupedProblem& p, cudaStream_t stream);
 
 }  // namespace moe

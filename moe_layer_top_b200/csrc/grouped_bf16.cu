@@ -385,38 +385,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               float* p = reinterpret_cast<float*>(smem) + 16 * c * kPartialPitch + row;
 #pragma unroll
               for (int i = 0; i < 16; ++i) p[i * kPartialPitch] = v[i];
-            } else if (args.out_f32) {
-              float* o = static_cast<float*>(args.out) + (static_cast<long long>(tl.n0) + 16 * c) * args.ldo + m;
-              if (m < args.m_rows) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                  if (i < n) o[i * args.ldo] = v[i];
-              }
             } else {
-              // four neighbouring lanes exchange what they have of four rows, so that each stores four columns of
-              // one: 8 bytes per lane, 64 bytes of each of four rows per instruction
-              uint32_t u[8], w[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const uint32_t mine = pack_bf16(v[2 * i], v[2 * i + 1]);  // rows 2 i and 2 i + 1 of this column
-                const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
-                u[i] = lane & 1 ? __byte_perm(other, mine, 0x7632) : __byte_perm(mine, other, 0x5410);
-              }
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const uint32_t got = __shfl_xor_sync(0xffffffffu, lane & 2 ? u[2 * j] : u[2 * j + 1], 2);
-                w[2 * j] = lane & 2 ? got : u[2 * j];
-                w[2 * j + 1] = lane & 2 ? u[2 * j + 1] : got;
-              }
-              const int r = lane & 3;  // this lane's rows: r + 4 j
-              __nv_bfloat16* o = static_cast<__nv_bfloat16*>(args.out) +
-                                 (static_cast<long long>(tl.n0) + 16 * c + r) * args.ldo + (m & ~3);
-              if (m < args.m_rows) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                  if (r + 4 * j < n)
-                    *reinterpret_cast<uint2*>(o + 4 * j * args.ldo) = make_uint2(w[2 * j], w[2 * j + 1]);
-              }
+              store_columns16(v, args.out, (static_cast<long long>(tl.n0) + 16 * c) * args.ldo, args.ldo, m, args.m_rows,
+                              n, args.out_f32);
             }
           }
         }

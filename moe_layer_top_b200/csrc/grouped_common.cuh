@@ -265,6 +265,18 @@ __device__ __forceinline__ uint4 pack_bf16x8(const float* f) {
   return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
 }
 
+// (a0, a1) <- (d0, d1) * (f0, f1) + (a0, a1), each correctly rounded; d as raw fp32 words
+__device__ __forceinline__ void ffma2v(float& a0, float& a1, uint32_t d0, uint32_t d1, float f0, float f1) {
+  asm("{\n\t.reg .b64 ra, rd, rf;\n\t"
+      "mov.b64 ra, {%0, %1};\n\t"
+      "mov.b64 rd, {%2, %3};\n\t"
+      "mov.b64 rf, {%4, %5};\n\t"
+      "fma.rn.f32x2 ra, rd, rf, ra;\n\t"
+      "mov.b64 {%0, %1}, ra;\n\t}"
+      : "+f"(a0), "+f"(a1)
+      : "r"(d0), "r"(d1), "f"(f0), "f"(f1));
+}
+
 __device__ __forceinline__ float4 load_in_cluster(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -272,6 +284,44 @@ __device__ __forceinline__ float4 load_in_cluster(uint32_t addr) {
                : "r"(addr)
                : "memory");
   return v;
+}
+
+// Stores 16 accumulator columns of tiles whose columns are output rows: lane `lane` holds column `col` of rows
+// 0 .. 15 at out[at + row * ldo + col], of which `rows` are stored, and columns below `cols` (a multiple of 8).  All
+// lanes of the warp take part.  bf16: four neighbouring lanes exchange what they have of four rows, so that each
+// stores four columns of one: 8 bytes per lane, 64 bytes of each of four rows per instruction.
+__device__ __forceinline__ void store_columns16(const float (&v)[16], void* out, long long at, long long ldo, int col,
+                                                int cols, int rows, bool f32) {
+  const int lane = threadIdx.x & 31;
+  if (f32) {
+    float* o = static_cast<float*>(out) + at + col;
+    if (col < cols) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (i < rows) o[i * ldo] = v[i];
+    }
+    return;
+  }
+  uint32_t u[8], w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t mine = pack_bf16(v[2 * i], v[2 * i + 1]);  // rows 2 i and 2 i + 1 of this column
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
+    u[i] = lane & 1 ? __byte_perm(other, mine, 0x7632) : __byte_perm(mine, other, 0x5410);
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, lane & 2 ? u[2 * j] : u[2 * j + 1], 2);
+    w[2 * j] = lane & 2 ? got : u[2 * j];
+    w[2 * j + 1] = lane & 2 ? u[2 * j + 1] : got;
+  }
+  const int r = lane & 3;  // this lane's rows: r + 4 j
+  __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out) + at + r * ldo + (col & ~3);
+  if (col < cols) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (r + 4 * j < rows) *reinterpret_cast<uint2*>(o + 4 * j * ldo) = make_uint2(w[2 * j], w[2 * j + 1]);
+  }
 }
 
 // The sum of a split tile: every CTA of the cluster has its partial sums [rows][kPartialPitch] at `smem`; CTA `cta`
