@@ -189,25 +189,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------------ producer (of each CTA)
-    if (lane == 0) {
-      const uint64_t pol = policy_evict_normal();
-      int stage = 0;
-      uint32_t phase = 0;
-      long long fills = 0;
-      bool ok = true;
-      for (int t = first_tile; t < num_tiles && ok; t += stride) {
-        const Tile tl = tile_at<Kind, Mode>(args, off, first, t);
-        const int m0 = tl.m0 + 128 * rank;
-        const int half = tl.n / C::kCtas;           // N columns that this CTA loads
-        const int n0 = tl.n0 + half * rank;
-        const int box = row_map_index(half);        // fwd, dx: one box holds them (dw: boxes of 64 columns)
-        const uint32_t bytes = C::kABytes + (Kind == kGroupedDw ? half : row_map_rows(box)) * 128;
-        const int k1 = red_end(tl);
-        for (int k = red_begin(tl); k < k1; k += 64) {
-          if (!wait_bar(&empty[stage], phase ^ 1u, abort_flag, args.status, kWhereGroupedProducer)) {
-            ok = false;
-            break;
-          }
+    const uint64_t pol = policy_evict_normal();
+    int stage = 0;
+    uint32_t phase = 0;
+    long long fills = 0;
+    bool ok = true;
+    for (int t = first_tile; t < num_tiles && ok; t += stride) {
+      const Tile tl = tile_at<Kind, Mode>(args, off, first, t);
+      const int m0 = tl.m0 + 128 * rank;
+      const int half = tl.n / C::kCtas;           // N columns that this CTA loads
+      const int n0 = tl.n0 + half * rank;
+      const int box = row_map_index(half);        // fwd, dx: one box holds them (dw: boxes of 64 columns)
+      const uint32_t bytes = C::kABytes + (Kind == kGroupedDw ? half : row_map_rows(box)) * 128;
+      const int k1 = red_end(tl);
+      for (int k = red_begin(tl); k < k1; k += 64) {
+        ok = warp_wait_bar(&empty[stage], phase ^ 1u, abort_flag, args.status, kWhereGroupedProducer);
+        if (!ok) break;
+        if (elect_lane()) {
           uint8_t* a = smem + static_cast<size_t>(stage) * C::kStageBytes;
           uint8_t* b = a + C::kABytes;
           uint32_t bar = smem_u32(&full[stage]);
@@ -223,42 +221,35 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if constexpr (Kind == kGroupedFwd) {
             load_3d<kPair>(a, &tm_a, bar, k, m0, tl.g, pol);
-          } else if constexpr (Kind == kGroupedDx) {
-            if (args.wide_a) {
-              load_4d<kPair>(a, &tm_a, bar, 0, k, m0 >> 6, tl.g, pol);
-            } else {
-              load_3d<kPair>(a, &tm_a, bar, m0, k, tl.g, pol);
-              load_3d<kPair>(a + 8192, &tm_a, bar, m0 + 64, k, tl.g, pol);
-            }
           } else {
+            const int y = tl.red0 + k, z = Kind == kGroupedDx ? tl.g : 0;
             if (args.wide_a) {
-              load_4d<kPair>(a, &tm_a, bar, 0, tl.red0 + k, m0 >> 6, 0, pol);
+              load_4d<kPair>(a, &tm_a, bar, 0, y, m0 >> 6, z, pol);
             } else {
-              load_3d<kPair>(a, &tm_a, bar, m0, tl.red0 + k, 0, pol);
-              load_3d<kPair>(a + 8192, &tm_a, bar, m0 + 64, tl.red0 + k, 0, pol);
+              load_3d<kPair>(a, &tm_a, bar, m0, y, z, pol);
+              load_3d<kPair>(a + 8192, &tm_a, bar, m0 + 64, y, z, pol);
             }
           }
-          if constexpr (Kind == kGroupedDw) {
-            if (args.wide_b) {
-              load_4d<kPair>(b, &tm_b.map[0], bar, 0, tl.red0 + k, n0 >> 6, 0, pol);
-            } else {
-              load_3d<kPair>(b, &tm_b.map[0], bar, n0, tl.red0 + k, 0, pol);
-              load_3d<kPair>(b + 8192, &tm_b.map[0], bar, n0 + 64, tl.red0 + k, 0, pol);
-            }
-          } else {
+          if constexpr (Kind != kGroupedDw) {
             load_2d<kPair>(b, &tm_b.map[box], bar, k, n0, pol);
-          }
-          ++fills;
-          if (++stage == C::kStages) {
-            stage = 0;
-            phase ^= 1u;
+          } else if (args.wide_b) {
+            load_4d<kPair>(b, &tm_b.map[0], bar, 0, tl.red0 + k, n0 >> 6, 0, pol);
+          } else {
+            load_3d<kPair>(b, &tm_b.map[0], bar, n0, tl.red0 + k, 0, pol);
+            load_3d<kPair>(b + 8192, &tm_b.map[0], bar, n0 + 64, tl.red0 + k, 0, pol);
           }
         }
+        __syncwarp();
+        ++fills;
+        if (++stage == C::kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
-      if (!ok && leader) drain_copies(full, C::kStages, fills);  // the leader's barriers count both CTAs' copies
     }
+    if (!ok && leader) drain_copies(full, C::kStages, fills);  // the leader's barriers count both CTAs' copies
   } else if (warp == 1) {
-    // ------------------------------------------------------------------ MMA issuer: the whole warp walks, lane 0 issues
+    // ------------------------------------------------------------------ MMA issuer
     int stage = 0, abuf = 0;
     uint32_t phase = 0, aphase = 0;
     uint32_t tails = 0;  // kTails: phase of each stage's tail barriers
@@ -305,12 +296,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           tc_fence_after();
-          if (lane == 0) {
+          if (elect_lane()) {
             const uint32_t a = smem_u32(st), b = a + C::kABytes;
-            for (int s = 0; s < steps; ++s) {
-              const uint64_t ad = C::kMnA ? smem_desc_mn_sw128(a + 2048 * s) : smem_desc_sw128(a + 32 * s);
-              const uint64_t bd = C::kMnB ? smem_desc_mn_sw128(b + 2048 * s) : smem_desc_sw128(b + 32 * s);
-              mma_bf16_for<kPair>(d, ad, bd, idesc, (k > k0 || s > 0) ? 1u : 0u);
+            const uint64_t ad = C::kMnA ? smem_desc_mn_sw128(a) : smem_desc_sw128(a);
+            const uint64_t bd = C::kMnB ? smem_desc_mn_sw128(b) : smem_desc_sw128(b);
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {  // 16 of the reduction further: 2048 bytes (MN-major) or 32
+              if (Kind == kGroupedDw && s >= steps) break;
+              mma_bf16_for<kPair>(d, ad + (C::kMnA ? 128 : 2) * s, bd + (C::kMnB ? 128 : 2) * s, idesc,
+                                  (k > k0 || s > 0) ? 1u : 0u);
             }
             commit_for<kPair>(&empty[stage]);
           }
@@ -318,7 +312,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           next_stage(1);
         }
         if (!ok) break;
-        if (lane == 0) commit_for<kPair>(&acc_full[abuf]);
+        if (elect_lane()) commit_for<kPair>(&acc_full[abuf]);
+        __syncwarp();
         abuf ^= 1;
         if (abuf == 0) aphase ^= 1u;
       }
@@ -336,10 +331,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         next_stage(1);
       }
     }
-    // every MMA this thread issued has completed once `drain` flips
+    // every MMA that the elected lane issued has completed once `drain` flips
     // (waited on even after an abort: TMEM must not be freed under a running MMA)
-    if (leader && lane == 0) {
-      commit_for<kPair>(drain);
+    if (leader) {
+      if (elect_lane()) commit_for<kPair>(drain);
+      __syncwarp();
       drain_mma(drain, args.status);
     }
   } else {

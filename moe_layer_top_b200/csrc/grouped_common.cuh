@@ -49,6 +49,19 @@ __device__ __forceinline__ bool warp_wait_bar(uint64_t* bar, uint32_t parity, vo
   return __all_sync(0xffffffffu, ok);
 }
 
+// One lane of a converged warp.  The producer and the issuer walk as whole warps and elect a lane for each batch of
+// instructions: what a warp computes alike then stays in uniform registers, where a loop inside `if (lane == 0)`
+// moves every descriptor and address there for each instruction (about 100 cycles per TMA or MMA instruction).
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // After an abort: let every copy already issued into the ring land before the CTA tears down.
 __device__ __forceinline__ void drain_copies(uint64_t* full, int stages, long long fills) {
   for (int s = 0; s < stages; ++s) {

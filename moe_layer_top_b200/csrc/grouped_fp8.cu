@@ -13,7 +13,7 @@
 // of the group the N side, which comes in steps of 16: a tile of a few rows
 // costs the tensor core little (a 128 x 128 tile of 2 rows held the memory
 // stream back: 512 rows over 256 groups of 7168 x 2048 took 613 us that way,
-// @C512@ this way).  An epilogue thread holds one column of up to 64 rows; the
+// 515 this way).  An epilogue thread holds one column of up to 64 rows; the
 // rows' factors are read from shared memory, the same for all lanes.
 // kSplit: a cluster of up to eight CTAs shares the K blocks of one such tile,
 // each leaves its partial sums in shared memory and all add a part of them
@@ -142,71 +142,72 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------------ producer
-    if (lane == 0) {
-      const uint64_t pol = policy_evict_normal();
-      int stage = 0;
-      uint32_t phase = 0;
-      long long fills = 0;
-      bool ok = true;
-      for (int t = first_tile; t < num_tiles && ok; t += stride) {
-        const Tile tl = tile_at(args, off, first, t);
-        const int box = row_map_index(tl.rows);  // rounded up to a multiple of 16 it still fits the box
-        const uint32_t bytes = row_map_rows(box) * 128 + 16384;
-        for (int kb = kb0; kb < kb1; ++kb) {
-          if (!wait_bar(&empty[stage], phase ^ 1u, abort_flag, args.status, kWhereGroupedProducer)) {
-            ok = false;
-            break;
-          }
+    const uint64_t pol = policy_evict_normal();
+    int stage = 0;
+    uint32_t phase = 0;
+    long long fills = 0;
+    bool ok = true;
+    for (int t = first_tile; t < num_tiles && ok; t += stride) {
+      const Tile tl = tile_at(args, off, first, t);
+      const int box = row_map_index(tl.rows);  // rounded up to a multiple of 16 it still fits the box
+      const uint32_t bytes = row_map_rows(box) * 128 + 16384;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        ok = warp_wait_bar(&empty[stage], phase ^ 1u, abort_flag, args.status, kWhereGroupedProducer);
+        if (!ok) break;
+        if (elect_lane()) {
           uint8_t* a = smem + static_cast<size_t>(stage) * kStageBytes;
           const uint32_t bar = smem_u32(&full[stage]);
           mbar_arrive_expect_tx(&full[stage], bytes);
           load_3d<false>(a, &tm_w, bar, kb * 128, tl.col0, tl.g, pol);
           load_2d<false>(a + 16384, &tm_x.map[box], bar, kb * 128, tl.row0, pol);
-          ++fills;
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1u;
-          }
+        }
+        __syncwarp();
+        ++fills;
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
-      if (!ok) drain_copies(full, kStages, fills);
     }
+    if (!ok) drain_copies(full, kStages, fills);
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      int stage = 0, abuf = 0;
-      uint32_t phase = 0, aphase = 0;
-      bool ok = true;
-      for (int t = first_tile; t < num_tiles && ok; t += stride) {
-        const Tile tl = tile_at(args, off, first, t);
-        const uint32_t idesc = make_idesc(kTile, 0, true) | (static_cast<uint32_t>(tl.n >> 3) << 17);
-        for (int kb = kb0; kb < kb1; ++kb) {
-          ok = wait_bar(&acc_empty[abuf], aphase ^ 1u, abort_flag, args.status, kWhereGroupedMma) &&
-               wait_bar(&full[stage], phase, abort_flag, args.status, kWhereGroupedMma);
-          if (!ok) break;
-          tc_fence_after();
+    int stage = 0, abuf = 0;
+    uint32_t phase = 0, aphase = 0;
+    bool ok = true;
+    for (int t = first_tile; t < num_tiles && ok; t += stride) {
+      const Tile tl = tile_at(args, off, first, t);
+      const uint32_t idesc = make_idesc(kTile, 0, true) | (static_cast<uint32_t>(tl.n >> 3) << 17);
+      for (int kb = kb0; kb < kb1; ++kb) {
+        ok = warp_wait_bar(&acc_empty[abuf], aphase ^ 1u, abort_flag, args.status, kWhereGroupedMma) &&
+             warp_wait_bar(&full[stage], phase, abort_flag, args.status, kWhereGroupedMma);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_lane()) {
           const uint32_t d = tmem_base + static_cast<uint32_t>(abuf * kTile);
-          const uint32_t a = smem_u32(smem + static_cast<size_t>(stage) * kStageBytes), b = a + 16384;
+          const uint32_t a = smem_u32(smem + static_cast<size_t>(stage) * kStageBytes);
+          const uint64_t ad = smem_desc_sw128(a), bd = smem_desc_sw128(a + 16384);
 #pragma unroll
-          for (int s = 0; s < 4; ++s)
-            mma_fp8(d, smem_desc_sw128(a + 32 * s), smem_desc_sw128(b + 32 * s), idesc, s > 0 ? 1u : 0u);
+          for (int s = 0; s < 4; ++s) mma_fp8(d, ad + 2 * s, bd + 2 * s, idesc, s > 0 ? 1u : 0u);  // + 32 bytes
           mma_commit(&acc_full[abuf]);
           mma_commit(&empty[stage]);
-          if (++abuf == kAccBufs) {
-            abuf = 0;
-            aphase ^= 1u;
-          }
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1u;
-          }
+        }
+        __syncwarp();
+        if (++abuf == kAccBufs) {
+          abuf = 0;
+          aphase ^= 1u;
+        }
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
-      // every MMA this thread issued has completed once `drain` flips
-      // (waited on even after an abort: TMEM must not be freed under a running MMA)
-      mma_commit(drain);
-      drain_mma(drain, args.status);
     }
+    // every MMA that the elected lanes issued has completed once `drain` flips
+    // (waited on even after an abort: TMEM must not be freed under a running MMA)
+    if (elect_lane()) mma_commit(drain);
+    __syncwarp();
+    drain_mma(drain, args.status);
   } else if (warp == 2) {
     // ------------------------------------------------------------------ factors
     int slot = 0;

@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
       // ---------------------------------------------------------------- producer (of each CTA)
       const uint64_t pol = policy_evict_normal();
       int stage = 0;
@@ -149,15 +149,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         const CUtensorMap* map = &tm_x.map[rows > 0 ? row_map_index(rows) : 0];
         const uint32_t bytes = (loaded(0) + loaded(1)) * 128 + 32768;
         for (int kb = 0; kb < kb_n; ++kb) {
-          if (!wait_bar(&empty[stage], phase ^ 1u, abort_flag, args.status, kWhereGroupedProducer)) {
-            ok = false;
-            break;
+          ok = warp_wait_bar(&empty[stage], phase ^ 1u, abort_flag, args.status, kWhereGroupedProducer);
+          if (!ok) break;
+          if (elect_lane()) {
+            uint8_t* a = smem + static_cast<size_t>(stage) * kStageBytes;
+            if (leader) mbar_arrive_expect_tx(&full[stage], bytes);
+            const uint32_t bar = in_cta(&full[stage], 0);
+            if (rows > 0) load_2d<true>(a, map, bar, kb * 128, tl.row0 + 128 * rank, pol);
+            load_3d<true>(a + 16384, &tm_w, bar, kb * 128, tl.col0 + 128 * rank, tl.g, pol);
           }
-          uint8_t* a = smem + static_cast<size_t>(stage) * kStageBytes;
-          if (leader) mbar_arrive_expect_tx(&full[stage], bytes);
-          const uint32_t bar = in_cta(&full[stage], 0);
-          if (rows > 0) load_2d<true>(a, map, bar, kb * 128, tl.row0 + 128 * rank, pol);
-          load_3d<true>(a + 16384, &tm_w, bar, kb * 128, tl.col0 + 128 * rank, tl.g, pol);
+          __syncwarp();
           ++fills;
           if (++stage == kStages) {
             stage = 0;
@@ -166,38 +167,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok && leader) drain_copies(full, kStages, fills);  // the leader's barriers count both CTAs' copies
-    } else if (warp == 1 && lane == 0 && leader) {
+    } else if (warp == 1) {
       // ---------------------------------------------------------------- MMA issuer
-      int stage = 0, abuf = 0;
-      uint32_t phase = 0, aphase = 0;
-      bool ok = true;
-      for (int t = first_tile; t < num_tiles && ok; t += stride) {
-        for (int kb = 0; kb < kb_n; ++kb) {
-          ok = wait_bar(&acc_empty[abuf], aphase ^ 1u, abort_flag, args.status, kWhereGroupedMma) &&
-               wait_bar(&full[stage], phase, abort_flag, args.status, kWhereGroupedMma);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t d = tmem_base + static_cast<uint32_t>(abuf * kTile);
-          const uint32_t a = smem_u32(smem + static_cast<size_t>(stage) * kStageBytes), b = a + 16384;
+      if (leader) {
+        int stage = 0, abuf = 0;
+        uint32_t phase = 0, aphase = 0;
+        bool ok = true;
+        for (int t = first_tile; t < num_tiles && ok; t += stride) {
+          for (int kb = 0; kb < kb_n; ++kb) {
+            ok = warp_wait_bar(&acc_empty[abuf], aphase ^ 1u, abort_flag, args.status, kWhereGroupedMma) &&
+                 warp_wait_bar(&full[stage], phase, abort_flag, args.status, kWhereGroupedMma);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_lane()) {
+              const uint32_t d = tmem_base + static_cast<uint32_t>(abuf * kTile);
+              const uint32_t a = smem_u32(smem + static_cast<size_t>(stage) * kStageBytes);
+              const uint64_t ad = smem_desc_sw128(a), bd = smem_desc_sw128(a + 16384);
 #pragma unroll
-          for (int s = 0; s < 4; ++s)
-            mma_fp8_for<true>(d, smem_desc_sw128(a + 32 * s), smem_desc_sw128(b + 32 * s), kIdesc, s > 0 ? 1u : 0u);
-          commit_for<true>(&acc_full[abuf]);
-          commit_for<true>(&empty[stage]);
-          if (++abuf == kAccBufs) {
-            abuf = 0;
-            aphase ^= 1u;
-          }
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1u;
+              for (int s = 0; s < 4; ++s) mma_fp8_for<true>(d, ad + 2 * s, bd + 2 * s, kIdesc, s > 0 ? 1u : 0u);
+              commit_for<true>(&acc_full[abuf]);
+              commit_for<true>(&empty[stage]);
+            }
+            __syncwarp();
+            if (++abuf == kAccBufs) {
+              abuf = 0;
+              aphase ^= 1u;
+            }
+            if (++stage == kStages) {
+              stage = 0;
+              phase ^= 1u;
+            }
           }
         }
+        // every MMA that the elected lanes issued has completed once `drain` flips
+        // (waited on even after an abort: TMEM must not be freed under a running MMA)
+        if (elect_lane()) commit_for<true>(drain);
+        __syncwarp();
+        drain_mma(drain, args.status);
       }
-      // every MMA this thread issued has completed once `drain` flips
-      // (waited on even after an abort: TMEM must not be freed under a running MMA)
-      commit_for<true>(drain);
-      drain_mma(drain, args.status);
     } else if (warp >= 2) {
       // ---------------------------------------------------------------- factors of column half warp - 2
       const int g = warp - 2;
