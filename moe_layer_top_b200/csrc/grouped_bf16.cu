@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tm_a);
-    tma_prefetch_desc(&tm_b.map[Kind == kGroupedDw ? 0 : 4]);
+    tma_prefetch_desc(&tm_b.map[0]);
   }
   if (warp == 1) tmem_alloc_for<kPair>(tmem_slot, C::kTmemCols);
   pdl_wait();
@@ -530,7 +530,7 @@ cudaError_t launch_tiles(const GroupedProblem& p, int splits, cudaStream_t s) {
   a.accumulate = p.accumulate;
   a.status = p.status;
   CUtensorMap tm_a, tm_out{};
-  RowMaps tm_b;
+  RowMaps tm_b{};
   long long tiles;
   bool ok;
   if constexpr (Kind == kGroupedDw) {
@@ -632,7 +632,8 @@ bool make_store_map(CUtensorMap* map, void* base, int batches, long long rows, l
 }
 
 bool make_row_maps(RowMaps* maps, const void* base, long long rows, long long cols, long long ld, int elem_bytes) {
-  for (int i = 0; i < 5; ++i)
+  const int most = row_map_index(rows < 128 ? static_cast<int>(rows) : 128);  // no tile has more rows than there are
+  for (int i = 0; i <= most; ++i)
     if (!make_grouped_map(&maps->map[i], base, 0, rows, cols, ld, elem_bytes, row_map_rows(i))) return false;
   return true;
 }

@@ -466,6 +466,7 @@ __host__ __device__ constexpr int row_map_index(int rows) {  // the smallest box
   return rows <= 16 ? 0 : (rows <= 32 ? 1 : (rows <= 64 ? 2 : (rows <= 96 ? 3 : 4)));
 }
 __host__ __device__ constexpr int row_map_rows(int index) { return index == 0 ? 16 : 32 * index; }
+// (those that M rows can need; a box beyond them is not described)
 bool make_row_maps(RowMaps* maps, const void* base, long long rows, long long cols, long long ld, int elem_bytes);
 
 // Once per kernel and device: allow its dynamic shared memory, and check that it is launched with at least `regs`

@@ -360,7 +360,7 @@ cudaError_t launch_columns(const GroupedProblem& p, int splits, cudaStream_t s) 
   a.ldo = p.ldo;
   a.out_f32 = p.out_f32;
   a.status = p.status;
-  RowMaps tm_x;
+  RowMaps tm_x{};
   CUtensorMap tm_w;
   if (!make_row_maps(&tm_x, p.a, p.M, p.K, p.lda, 1) || !make_grouped_map(&tm_w, p.b, p.G, p.N, p.K, p.K, 1, 128))
     return cudaErrorInvalidValue;

@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
-    tma_prefetch_desc(&tm_x.map[4]);
+    tma_prefetch_desc(&tm_x.map[0]);
     tma_prefetch_desc(&tm_w);
   }
   if (warp == 1) tmem_alloc_for<true>(tmem_slot, kTmemCols);
@@ -404,7 +404,7 @@ cudaError_t launch_grouped_fp8_pair(const GroupedProblem& p, cudaStream_t s) {
   a.ldo = p.ldo;
   a.out_f32 = p.out_f32;
   a.status = p.status;
-  RowMaps tm_x;
+  RowMaps tm_x{};
   CUtensorMap tm_w, tm_out;
   if (!make_row_maps(&tm_x, p.a, p.M, p.K, p.lda, 1) ||
       !make_grouped_map(&tm_w, p.b, p.G, p.N, p.K, p.K, 1, 128) ||

@@ -418,36 +418,45 @@ def combine_reduce_scatter_emulated(T, topk, H, ranks, epoch, timeout_us=2_000_0
 _OUT_DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_FP32}
 
 
-def _require(name: str, t, dtype, shape, device, rows=False):
-    """``t`` is a CUDA tensor of this type, shape and device: contiguous, or (``rows``) with unit stride along
-    its last dimension."""
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device and t.is_cuda
-            and (t.is_contiguous() or (rows and t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] == 1)))):
-        return t
+def _refuse(name, t, dtype, shape, device, rows):
+    """Raise for a tensor that is not what ``_rows`` or ``_flat`` needs."""
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name}: a tensor is needed, got {type(t).__name__}")
     if t.dtype != dtype:
         raise ValueError(f"{name}: type {t.dtype}, {dtype} is needed")
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{name}: on {t.device}, needed on the CUDA device of the first argument ({device})")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, needed on the device of the first argument ({device})")
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, {tuple(shape)} is needed")
     raise ValueError(f"{name}: " + ("its last dimension must have stride 1" if rows else "must be contiguous"))
 
 
-def _2d(name: str, t):
-    if not isinstance(t, torch.Tensor) or t.dim() != 2:
-        raise ValueError(f"{name}: a 2-dimensional tensor is needed")
+def _rows(name, t, dtype, shape, device):
+    """(address, elements between rows) of a 2-D tensor of this type, shape and device whose rows are contiguous (a
+    single row's stride says nothing)."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device):
+        _refuse(name, t, dtype, shape, device, True)
+    ld, one = t.stride()
+    if one != 1 and shape[1] > 1:
+        _refuse(name, t, dtype, shape, device, True)
+    return t.data_ptr(), ld if shape[0] > 1 else shape[1]
+
+
+def _flat(name, t, dtype, shape, device):
+    """The address of a contiguous tensor of this type, shape and device."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device
+            and t.is_contiguous()):
+        _refuse(name, t, dtype, shape, device, False)
+    return t.data_ptr()
+
+
+def _sizes(name, t, dims=2):
+    """The sizes of a call's first argument, a CUDA tensor."""
+    if not isinstance(t, torch.Tensor) or t.dim() != dims:
+        raise ValueError(f"{name}: a {dims}-dimensional tensor is needed")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: on {t.device}, a CUDA tensor is needed")
     return t.shape
-
-
-def _ld(t) -> int:
-    """Elements between the rows of a 2-D tensor (a single row's stride says nothing)."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
 
 
 def _run(fn, device, stream, *args):
@@ -457,14 +466,9 @@ def _run(fn, device, stream, *args):
     if index != torch._C._cuda_getDevice():
         with torch.cuda.device(device):
             return _run(fn, device, stream, *args)
-    _check(fn(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream))
-
-
-def _out(name, out, shape, dtype, device):
-    """``out`` checked, or a new tensor."""
-    if out is None:
-        return torch.empty(*shape, dtype=dtype, device=device)
-    return _require(name, out, dtype, shape, device, True)
+    rc = fn(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc)
 
 
 def _like(x, dtype=None):
@@ -472,12 +476,27 @@ def _like(x, dtype=None):
     return torch.empty_like(x, dtype=dtype, memory_format=torch.contiguous_format)
 
 
-def _out_dtype(out, out_dtype):
-    dtype = out_dtype if out is None or out_dtype is not None else out.dtype
-    dtype = torch.bfloat16 if dtype is None else dtype
+def _out(out, out_dtype, rows, cols, like):
+    """The output of a product, new or checked: (tensor, address, elements between rows, type's number)."""
+    dtype = out_dtype or (torch.bfloat16 if out is None else out.dtype)
     if dtype not in _OUT_DTYPES:
         raise ValueError(f"out_dtype: {dtype}, torch.bfloat16 or torch.float32 is needed")
-    return dtype
+    if out is None:
+        out = torch.empty(rows, cols, dtype=dtype, device=like.device)
+        return out, out.data_ptr(), cols, _OUT_DTYPES[dtype]
+    return out, *_rows("out", out, dtype, (rows, cols), like.device), _OUT_DTYPES[dtype]
+
+
+def _status(status, dev):
+    return None if status is None else _flat("status", status, torch.int32, (1,), dev)
+
+
+def _offsets(offsets, G, dev):
+    if offsets is None:
+        if G != 1:
+            raise ValueError(f"offsets: needed for {G} groups")
+        return None
+    return _flat("offsets", offsets, torch.int32, (G + 1,), dev)
 
 
 def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, *, residual=None, residual_out=None, y=True,
@@ -488,27 +507,38 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, *, residu
     residual itself; None without residual), ``y`` (bf16 [T, H]; True allocates it, a tensor receives it, False
     leaves it out), ``codes`` and ``scales`` (with ``fp8``: the FP8 rows of y, uint8 [T, H] and fp32
     [ceil(H / 128), T]) and ``rstd`` (fp32 [T] if asked for)."""
-    T, H = _2d("x", x)
-    dev = x.device
-    _require("x", x, torch.bfloat16, (T, H), dev, True)
-    _require("weight", weight, torch.bfloat16, (H,), dev)
+    shape = T, H = _sizes("x", x)
+    dev, bf16 = x.device, torch.bfloat16
+    x_p, x_ld = _rows("x", x, bf16, shape, dev)
+    w_p = _flat("weight", weight, bf16, (H,), dev)
+    r_p = r_ld = o_p = o_ld = y_p = y_ld = c_p = s_p = rstd_p = codes = scales = None
     if residual is not None:
-        _require("residual", residual, torch.bfloat16, (T, H), dev, True)
-        residual_out = _like(x) if residual_out is None else _require("residual_out", residual_out, torch.bfloat16,
-                                                                       (T, H), dev, True)
+        r_p, r_ld = _rows("residual", residual, bf16, shape, dev)
+        if residual_out is None:
+            residual_out = _like(x)
+            o_p, o_ld = residual_out.data_ptr(), H
+        else:
+            o_p, o_ld = _rows("residual_out", residual_out, bf16, shape, dev)
     elif residual_out is not None:
         raise ValueError("residual_out: given without residual")
-    if y is True or y is False or y is None:
-        y = _like(x) if y else None
+    if y is True:
+        y = _like(x)
+        y_p, y_ld = y.data_ptr(), H
+    elif y is False or y is None:
+        y = None
     else:
-        _require("y", y, torch.bfloat16, (T, H), dev, True)
-    codes = _like(x, torch.uint8) if fp8 else None
-    scales = x.new_empty(((H + 127) // 128, T), dtype=torch.float32) if fp8 else None
-    r = x.new_empty(T, dtype=torch.float32) if rstd else None
-    _run(lib().moe_rms_norm, dev, stream, _addr(x), _ld(x), _addr(residual), 0 if residual is None else _ld(residual),
-         _addr(residual_out), 0 if residual is None else _ld(residual_out), _addr(weight), eps, T, H, _addr(y),
-         0 if y is None else _ld(y), _addr(codes), _addr(scales), _addr(r))
-    return {"residual": residual_out, "y": y, "codes": codes, "scales": scales, "rstd": r}
+        y_p, y_ld = _rows("y", y, bf16, shape, dev)
+    if fp8:
+        codes = _like(x, torch.uint8)
+        scales = torch.empty((H + 127) // 128, T, dtype=torch.float32, device=dev)
+        c_p, s_p = codes.data_ptr(), scales.data_ptr()
+    if rstd:
+        rstd = x.new_empty(T, dtype=torch.float32)
+        rstd_p = rstd.data_ptr()
+    _run(lib().moe_rms_norm, dev, stream, x_p, x_ld, r_p, r_ld or 0, o_p, o_ld or 0, w_p, eps, T, H, y_p, y_ld or 0,
+         c_p, s_p, rstd_p)
+    return {"residual": residual_out, "y": y, "codes": codes, "scales": scales,
+            "rstd": rstd if rstd_p is not None else None}
 
 
 def rms_norm_backward(dy: torch.Tensor, s: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor, *, dresidual=None,
@@ -518,81 +548,69 @@ def rms_norm_backward(dy: torch.Tensor, s: torch.Tensor, weight: torch.Tensor, r
     ``s`` is what was normalised (x, or the ``residual`` that the forward pass returned), ``dresidual`` the
     gradient that reaches it by other ways; ``ws`` a uint8 workspace of
     ``moe_rms_norm_backward_workspace_size`` bytes (allocated if not given)."""
-    T, H = _2d("dy", dy)
-    dev = dy.device
-    _require("dy", dy, torch.bfloat16, (T, H), dev, True)
-    _require("s", s, torch.bfloat16, (T, H), dev, True)
-    _require("weight", weight, torch.bfloat16, (H,), dev)
-    _require("rstd", rstd, torch.float32, (T,), dev)
-    if dresidual is not None:
-        _require("dresidual", dresidual, torch.bfloat16, (T, H), dev, True)
-    dx = _like(dy) if dx is None else _require("dx", dx, torch.bfloat16, (T, H), dev, True)
-    dweight = dy.new_empty(H, dtype=torch.float32)
-    if ws is None:
-        ws = dy.new_empty(max(int(lib().moe_rms_norm_backward_workspace_size(T, H)), 16), dtype=torch.uint8)
+    shape = T, H = _sizes("dy", dy)
+    dev, bf16 = dy.device, torch.bfloat16
+    dy_p, dy_ld = _rows("dy", dy, bf16, shape, dev)
+    s_p, s_ld = _rows("s", s, bf16, shape, dev)
+    w_p = _flat("weight", weight, bf16, (H,), dev)
+    rstd_p = _flat("rstd", rstd, torch.float32, (T,), dev)
+    r_p, r_ld = (None, 0) if dresidual is None else _rows("dresidual", dresidual, bf16, shape, dev)
+    if dx is None:
+        dx = _like(dy)
+        dx_p, dx_ld = dx.data_ptr(), H
     else:
-        _require("ws", ws, torch.uint8, ws.shape, dev)
-    _run(lib().moe_rms_norm_backward, dev, stream, _addr(dy), _ld(dy), _addr(s), _ld(s), _addr(weight), _addr(rstd),
-         _addr(dresidual), 0 if dresidual is None else _ld(dresidual), T, H, _addr(dx), _ld(dx), _addr(dweight), _addr(ws),
-         ws.numel())
+        dx_p, dx_ld = _rows("dx", dx, bf16, shape, dev)
+    dweight = dy.new_empty(H, dtype=torch.float32)
+    L = lib()
+    if ws is None:
+        ws = dy.new_empty(max(L.moe_rms_norm_backward_workspace_size(T, H), 16), dtype=torch.uint8)
+    else:
+        _flat("ws", ws, torch.uint8, ws.shape, dev)
+    _run(L.moe_rms_norm_backward, dev, stream, dy_p, dy_ld, s_p, s_ld, w_p, rstd_p, r_p, r_ld, T, H, dx_p, dx_ld,
+         dweight.data_ptr(), ws.data_ptr(), ws.numel())
     return dx, dweight
 
 
 def quantize_rows_fp8(x: torch.Tensor, stream=None):
     """bf16 [rows, cols] -> FP8 rows: (E4M3 codes as uint8 [rows, cols], fp32 scales [ceil(cols / 128), rows])."""
-    rows, cols = _2d("x", x)
-    _require("x", x, torch.bfloat16, (rows, cols), x.device, True)
+    shape = rows, cols = _sizes("x", x)
+    dev = x.device
+    x_p, x_ld = _rows("x", x, torch.bfloat16, shape, dev)
     codes = _like(x, torch.uint8)
-    scales = x.new_empty(((cols + 127) // 128, rows), dtype=torch.float32)
-    _run(lib().moe_quantize_rows_fp8, x.device, stream, _addr(x), _ld(x), rows, cols, _addr(codes), _addr(scales))
+    scales = torch.empty((cols + 127) // 128, rows, dtype=torch.float32, device=dev)
+    _run(lib().moe_quantize_rows_fp8, dev, stream, x_p, x_ld, rows, cols, codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
 
 def dequantize_rows_fp8(codes: torch.Tensor, scales: torch.Tensor, *, out=None, stream=None):
     """FP8 rows -> the bf16 [rows, cols] values that they stand for."""
-    rows, cols = _2d("codes", codes)
+    shape = rows, cols = _sizes("codes", codes)
     dev = codes.device
-    _require("codes", codes, torch.uint8, (rows, cols), dev)
-    _require("scales", scales, torch.float32, ((cols + 127) // 128, rows), dev)
-    out = _like(codes, torch.bfloat16) if out is None else _require("out", out, torch.bfloat16, (rows, cols), dev, True)
-    _run(lib().moe_dequantize_rows_fp8, dev, stream, _addr(codes), _addr(scales), rows, cols, _addr(out), _ld(out))
+    c_p = _flat("codes", codes, torch.uint8, shape, dev)
+    s_p = _flat("scales", scales, torch.float32, ((cols + 127) // 128, rows), dev)
+    if out is None:
+        out = _like(codes, torch.bfloat16)
+        o_p, o_ld = out.data_ptr(), cols
+    else:
+        o_p, o_ld = _rows("out", out, torch.bfloat16, shape, dev)
+    _run(lib().moe_dequantize_rows_fp8, dev, stream, c_p, s_p, rows, cols, o_p, o_ld)
     return out
-
-
-def _weight(name, w, dtype, dev):
-    if not isinstance(w, torch.Tensor) or w.dim() != 3:
-        raise ValueError(f"{name}: a 3-dimensional tensor [groups, N, K] is needed")
-    return _require(name, w, dtype, w.shape, dev).shape
-
-
-def _offsets(offsets, G, dev):
-    if offsets is None:
-        if G != 1:
-            raise ValueError(f"offsets: needed for {G} groups")
-        return None
-    return _require("offsets", offsets, torch.int32, (G + 1,), dev)
 
 
 def matmul_fp8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, *, out=None,
                out_dtype=None, status=None, stream=None):
     """y [M, N] = x . w^T of FP8 rows x [M, K] (codes and scales of :func:`quantize_rows_fp8` or
     :func:`rms_norm`) and a weight w [N, K] with one scale per 128 x 128 block; bf16 or fp32."""
-    M, K = _2d("x", x)
-    N = _2d("w", w)[0]
-    dev = x.device
-    _require("x", x, torch.uint8, (M, K), dev)
-    _require("x_scale", x_scale, torch.float32, ((K + 127) // 128, M), dev)
-    _require("w", w, torch.uint8, (N, K), dev)
-    _require("w_scale", w_scale, torch.float32, ((N + 127) // 128, (K + 127) // 128), dev)
-    dtype = _out_dtype(out, out_dtype)
-    out = _out("out", out, (M, N), dtype, dev)
-    _run(lib().moe_matmul_fp8, dev, stream, _addr(x), _addr(x_scale), _addr(w), _addr(w_scale), M, N, K, _addr(out),
-         _ld(out), _OUT_DTYPES[dtype], _status(status, dev))
+    M, K = _sizes("x", x)
+    N = _sizes("w", w)[0]
+    dev, kb = x.device, (K + 127) // 128
+    x_p = _flat("x", x, torch.uint8, (M, K), dev)
+    xs_p = _flat("x_scale", x_scale, torch.float32, (kb, M), dev)
+    w_p = _flat("w", w, torch.uint8, (N, K), dev)
+    ws_p = _flat("w_scale", w_scale, torch.float32, ((N + 127) // 128, kb), dev)
+    out, o_p, o_ld, dtype = _out(out, out_dtype, M, N, x)
+    _run(lib().moe_matmul_fp8, dev, stream, x_p, xs_p, w_p, ws_p, M, N, K, o_p, o_ld, dtype, _status(status, dev))
     return out
-
-
-def _status(status, dev):
-    return None if status is None else _addr(_require("status", status, torch.int32, (1,), dev))
 
 
 def grouped_matmul(x: torch.Tensor, w: torch.Tensor, offsets, *, x_scale=None, w_scale=None, out=None, out_dtype=None,
@@ -602,41 +620,42 @@ def grouped_matmul(x: torch.Tensor, w: torch.Tensor, offsets, *, x_scale=None, w
     x [M, K] bf16 and w [G, N, K] bf16; or FP8 rows x with ``x_scale`` [ceil(K / 128), M] and E4M3 weights with
     ``w_scale`` [G, ceil(N / 128), ceil(K / 128)].  ``offsets`` int32 [G + 1] on the device (None: one group of
     all rows).  y [M, N] bf16 or fp32; rows of no group are not written."""
-    M, K = _2d("x", x)
+    M, K = _sizes("x", x)
+    G, N, _ = _sizes("w", w, 3)
     dev = x.device
     if (x_scale is None) != (w_scale is None):
         raise ValueError("x_scale and w_scale: give both (FP8) or neither (bf16)")
-    fp8 = x_scale is not None
-    G, N, _ = _weight("w", w, torch.uint8 if fp8 else torch.bfloat16, dev)
-    _require("w", w, w.dtype, (G, N, K), dev)
-    _require("x", x, torch.uint8 if fp8 else torch.bfloat16, (M, K), dev, not fp8)
-    _offsets(offsets, G, dev)
-    dtype = _out_dtype(out, out_dtype)
-    out = _out("out", out, (M, N), dtype, dev)
-    if fp8:
-        _require("x_scale", x_scale, torch.float32, ((K + 127) // 128, M), dev)
-        _require("w_scale", w_scale, torch.float32, (G, (N + 127) // 128, (K + 127) // 128), dev)
-        _run(lib().moe_grouped_matmul_fp8, dev, stream, _addr(x), _addr(x_scale), _addr(w), _addr(w_scale), _addr(offsets),
-             M, G, N, K, _addr(out), _ld(out), _OUT_DTYPES[dtype], _status(status, dev))
-    else:
-        _run(lib().moe_grouped_matmul, dev, stream, _addr(x), _ld(x), _addr(w), _addr(offsets), M, G, N, K, _addr(out),
-             _ld(out), _OUT_DTYPES[dtype], _status(status, dev))
+    off_p = _offsets(offsets, G, dev)
+    if x_scale is None:
+        x_p, x_ld = _rows("x", x, torch.bfloat16, (M, K), dev)
+        w_p = _flat("w", w, torch.bfloat16, (G, N, K), dev)
+        out, o_p, o_ld, dtype = _out(out, out_dtype, M, N, x)
+        _run(lib().moe_grouped_matmul, dev, stream, x_p, x_ld, w_p, off_p, M, G, N, K, o_p, o_ld, dtype,
+             _status(status, dev))
+        return out
+    kb = (K + 127) // 128
+    x_p = _flat("x", x, torch.uint8, (M, K), dev)
+    w_p = _flat("w", w, torch.uint8, (G, N, K), dev)
+    xs_p = _flat("x_scale", x_scale, torch.float32, (kb, M), dev)
+    ws_p = _flat("w_scale", w_scale, torch.float32, (G, (N + 127) // 128, kb), dev)
+    out, o_p, o_ld, dtype = _out(out, out_dtype, M, N, x)
+    _run(lib().moe_grouped_matmul_fp8, dev, stream, x_p, xs_p, w_p, ws_p, off_p, M, G, N, K, o_p, o_ld, dtype,
+         _status(status, dev))
     return out
 
 
 def grouped_matmul_dx(dy: torch.Tensor, w: torch.Tensor, offsets, *, out=None, out_dtype=None, status=None,
                       stream=None):
     """Gradient of :func:`grouped_matmul`'s rows: dx[r] = dy[r] . w[g] (dy [M, N], w [G, N, K] bf16 -> [M, K])."""
-    M, N = _2d("dy", dy)
+    M, N = _sizes("dy", dy)
+    G, _, K = _sizes("w", w, 3)
     dev = dy.device
-    G, _, K = _weight("w", w, torch.bfloat16, dev)
-    _require("w", w, torch.bfloat16, (G, N, K), dev)
-    _require("dy", dy, torch.bfloat16, (M, N), dev, True)
-    _offsets(offsets, G, dev)
-    dtype = _out_dtype(out, out_dtype)
-    out = _out("out", out, (M, K), dtype, dev)
-    _run(lib().moe_grouped_matmul_dx, dev, stream, _addr(dy), _ld(dy), _addr(w), _addr(offsets), M, G, N, K, _addr(out),
-         _ld(out), _OUT_DTYPES[dtype], _status(status, dev))
+    dy_p, dy_ld = _rows("dy", dy, torch.bfloat16, (M, N), dev)
+    w_p = _flat("w", w, torch.bfloat16, (G, N, K), dev)
+    off_p = _offsets(offsets, G, dev)
+    out, o_p, o_ld, dtype = _out(out, out_dtype, M, K, dy)
+    _run(lib().moe_grouped_matmul_dx, dev, stream, dy_p, dy_ld, w_p, off_p, M, G, N, K, o_p, o_ld, dtype,
+         _status(status, dev))
     return out
 
 
@@ -644,20 +663,23 @@ def grouped_matmul_dw(dy: torch.Tensor, x: torch.Tensor, offsets, *, out=None, o
                       status=None, stream=None):
     """Gradient of :func:`grouped_matmul`'s weights: dw[g] = sum of dy[r]^T x[r] over the group's rows (dy [M, N],
     x [M, K] bf16 -> [G, N, K] bf16 or fp32; zero for an empty group).  ``accumulate`` adds to an fp32 ``out``."""
-    M, N = _2d("dy", dy)
-    K = _2d("x", x)[1]
+    M, N = _sizes("dy", dy)
+    K = _sizes("x", x)[1]
     dev = dy.device
-    _require("dy", dy, torch.bfloat16, (M, N), dev, True)
-    _require("x", x, torch.bfloat16, (M, K), dev, True)
+    dy_p, dy_ld = _rows("dy", dy, torch.bfloat16, (M, N), dev)
+    x_p, x_ld = _rows("x", x, torch.bfloat16, (M, K), dev)
     G = 1 if offsets is None else offsets.numel() - 1
-    _offsets(offsets, G, dev)
+    off_p = _offsets(offsets, G, dev)
     if accumulate and out is None:
         raise ValueError("accumulate: needs out")
-    dtype = _out_dtype(out, out_dtype)
+    dtype = out_dtype or (torch.bfloat16 if out is None else out.dtype)
+    if dtype not in _OUT_DTYPES:
+        raise ValueError(f"out_dtype: {dtype}, torch.bfloat16 or torch.float32 is needed")
     if out is None:
         out = torch.empty(G, N, K, dtype=dtype, device=dev)
+        o_p = out.data_ptr()
     else:
-        _require("out", out, dtype, (G, N, K), dev)
-    _run(lib().moe_grouped_matmul_dw, dev, stream, _addr(dy), _ld(dy), _addr(x), _ld(x), _addr(offsets), M, G, N, K,
-         _addr(out), _OUT_DTYPES[dtype], 1 if accumulate else 0, _status(status, dev))
+        o_p = _flat("out", out, dtype, (G, N, K), dev)
+    _run(lib().moe_grouped_matmul_dw, dev, stream, dy_p, dy_ld, x_p, x_ld, off_p, M, G, N, K, o_p, _OUT_DTYPES[dtype],
+         1 if accumulate else 0, _status(status, dev))
     return out
