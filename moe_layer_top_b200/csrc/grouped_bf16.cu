@@ -68,8 +68,9 @@ struct Cfg {
   static constexpr bool kMnA = Kind != kGroupedFwd;
   static constexpr bool kMnB = Kind == kGroupedDw;
   static constexpr int kTmemCols = 2 * kNTile;
-  // dw: each epilogue warp stages boxes of 32 rows x 128 bytes for TMA stores
-  static constexpr int kOutBytes = Kind == kGroupedDw && Mode != kModeSplit ? kGroupedEpiWarps * 4096 : 0;
+  // dw: each epilogue warp stages boxes of 32 rows x 64 bytes for TMA stores (128 bytes would cost a stage of the
+  // ring, and the short reductions need them: dw of 32768 rows over 128 experts 526 us with five, 507 with six)
+  static constexpr int kOutBytes = Kind == kGroupedDw && Mode != kModeSplit ? kGroupedEpiWarps * 2048 : 0;
   static constexpr int kStages = (kSmemMax - 1024 - kGroupedReserve - kOutBytes) / kStageBytes;
   static constexpr size_t kSmemBytes =
       static_cast<size_t>(kStages) * kStageBytes + kOutBytes + kGroupedReserve + 1024;
@@ -344,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int g = (warp - 2) >> 2;        // the two groups share the accumulator's columns
     const int row = 32 * q + lane;        // accumulator row
     const uint32_t lane_addr = static_cast<uint32_t>(32 * q) << 16;
-    uint8_t* out_box = staging + static_cast<size_t>(warp - 2) * 4096;
+    uint8_t* out_box = staging + static_cast<size_t>(warp - 2) * 2048;
     const uint32_t empty_bar = kPair ? in_cta(acc_empty, 0) : smem_u32(acc_empty);
     int abuf = 0;
     uint32_t aphase = 0;
@@ -393,10 +394,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) arrive_in_cluster(empty_bar + 8 * abuf);
         }
       } else {
-        // a lane holds a row: 128 bytes of each go through shared memory as one TMA store of the warp's 32 rows
+        // a lane holds a row: 64 bytes of each go through shared memory as one TMA store of the warp's 32 rows
         // (it leaves out what lies behind the last row and column)
         constexpr int kCols = C::kNTile / 2;  // columns of this group
-        const int step = args.out_f32 ? 32 : 64;
+        const int step = args.out_f32 ? 16 : 32;
         // a group without rows adds nothing to an accumulated gradient
         const int end = live && !(args.accumulate && tl.red == 0) ? min(kCols, tl.valid - g * kCols) : 0;
         if constexpr (kSplit) {
@@ -419,8 +420,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int c = 0; !kSplit && c < end; c += step) {
           const int col = g * kCols + c;
-          uint4 piece[8];
+          uint4 piece[4];
           if (args.out_f32) {
+            uint32_t v[16];
+            if (any) {
+              tmem_ld16u(d + col, v);
+              tmem_wait_ld();
+              pin16(v);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] = 0u;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) piece[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          } else {
             uint32_t v[32];
             if (any) {
               tmem_ld32(d + col, v);
@@ -431,24 +444,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int i = 0; i < 32; ++i) v[i] = 0u;
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) piece[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-          } else {
-            uint32_t v[2][32];
-            if (any) {
-              tmem_ld32(d + col, v[0]);
-              tmem_ld32(d + col + 32, v[1]);
-              tmem_wait_ld();
-              pin32(v[0]);
-              pin32(v[1]);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[0][i] = v[1][i] = 0u;
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < 4; ++i) {
               float f[8];
 #pragma unroll
-              for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(v[i / 4][8 * (i & 3) + j]);
+              for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(v[8 * i + j]);
               piece[i] = pack_bf16x8(f);
             }
           }
@@ -544,7 +543,7 @@ cudaError_t launch_tiles(const GroupedProblem& p, int splits, cudaStream_t s) {
     ok = (a.wide_a ? make_wide_map(&tm_a, dy, 1, rows, p.N, lddy) : make_grouped_map(&tm_a, dy, 1, rows, p.N, lddy, 2, 64)) &&
          (a.wide_b ? make_wide_map(&tm_b.map[0], x, 1, rows, p.K, ldx)
                    : make_grouped_map(&tm_b.map[0], x, 1, rows, p.K, ldx, 2, 64)) &&
-         make_store_map(&tm_out, p.out, p.G, p.N, p.K, p.K, p.out_f32);
+         make_store_map(&tm_out, p.out, p.G, p.N, p.K, p.K, p.out_f32, 64);
     tiles = static_cast<long long>(p.G) * a.m_tiles * a.n_tiles;
   } else {
     a.wide_a = Kind == kGroupedDx && p.K % 64 == 0;
@@ -586,7 +585,8 @@ cudaError_t dispatch(const GroupedProblem& p, cudaStream_t s) {
 namespace {
 
 bool encode(CUtensorMap* map, CUtensorMapDataType type, int dims, const void* base, const cuuint64_t* size,
-            const cuuint64_t* strides, const cuuint32_t* box) {
+            const cuuint64_t* strides, const cuuint32_t* box,
+            CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   if (fn == nullptr) {
     void* p = nullptr;
@@ -598,7 +598,7 @@ bool encode(CUtensorMap* map, CUtensorMapDataType type, int dims, const void* ba
   }
   const cuuint32_t one[4] = {1, 1, 1, 1};
   return fn(map, type, dims, const_cast<void*>(base), size, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -622,13 +622,14 @@ bool make_wide_map(CUtensorMap* map, const void* base, int batches, long long ro
   return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, size, strides, box);
 }
 
-bool make_store_map(CUtensorMap* map, void* base, int batches, long long rows, long long cols, long long ld, bool f32) {
+bool make_store_map(CUtensorMap* map, void* base, int batches, long long rows, long long cols, long long ld, bool f32,
+                    int box_bytes) {
   const long long elem = f32 ? 4 : 2;
   const cuuint64_t size[3] = {u64(cols), u64(rows), u64(batches)};
   const cuuint64_t strides[2] = {u64(ld * elem), u64(ld * rows * elem)};
-  const cuuint32_t box[3] = {f32 ? 32u : 64u, 32, 1};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_bytes / elem), 32, 1};
   return encode(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, size, strides,
-                box);
+                box, box_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 bool make_row_maps(RowMaps* maps, const void* base, long long rows, long long cols, long long ld, int elem_bytes) {

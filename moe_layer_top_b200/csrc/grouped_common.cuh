@@ -247,11 +247,14 @@ __device__ __forceinline__ void store_3d(const void* map, const void* src, int x
                  : "memory");
 }
 
-// Row `lane` of a warp's 32 x 128-byte staging box, as the 128-byte swizzle lays it out: 16-byte piece c goes to
-// c ^ (lane mod 8), so that the lanes of a store spread over all banks.
-__device__ __forceinline__ void stage_row(uint8_t* box, int lane, const uint4 (&piece)[8]) {
+// Row `lane` of a warp's staging box of 32 rows x 16 kPieces bytes (128 or 64), as the swizzle of that width lays it out:
+// 16-byte piece c of row r goes to c ^ (r mod 8), or c ^ (r / 2 mod 4), so that a store's lanes spread over all banks.
+template <int kPieces>
+__device__ __forceinline__ void stage_row(uint8_t* box, int lane, const uint4 (&piece)[kPieces]) {
+  static_assert(kPieces == 8 || kPieces == 4, "swizzle width");
+  const int x = kPieces == 8 ? lane & 7 : (lane >> 1) & 3;
 #pragma unroll
-  for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(box + lane * 128 + ((c ^ (lane & 7)) << 4)) = piece[c];
+  for (int c = 0; c < kPieces; ++c) *reinterpret_cast<uint4*>(box + lane * 16 * kPieces + ((c ^ x) << 4)) = piece[c];
 }
 
 // Values that an asynchronous TMEM load delivers may be used from here on: placed behind tcgen05.wait::ld, it keeps the
@@ -444,8 +447,10 @@ __device__ __forceinline__ int group_of_tile(const int* first, int G, int t) {
 // --------------------------------------------------------------------------
 // host side
 // --------------------------------------------------------------------------
-// tensor map of an output [batches, rows, cols] (bf16 or fp32) for store_3d: boxes of 128 bytes x 32 rows
-bool make_store_map(CUtensorMap* map, void* base, int batches, long long rows, long long cols, long long ld, bool f32);
+// tensor map of an output [batches, rows, cols] (bf16 or fp32) for store_3d: boxes of 128 or 64 bytes x 32 rows, with
+// the swizzle of that width
+bool make_store_map(CUtensorMap* map, void* base, int batches, long long rows, long long cols, long long ld, bool f32,
+                    int box_bytes);
 
 // tensor map of bf16 [batches, rows, cols] whose box is 64 rows of 2 x 64 columns, the second 64 columns 8192 bytes
 // behind the first (dimensions: column in a run of 64, row, run, batch); cols must be a multiple of 64

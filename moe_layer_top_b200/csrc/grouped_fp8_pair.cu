@@ -408,7 +408,7 @@ cudaError_t launch_grouped_fp8_pair(const GroupedProblem& p, cudaStream_t s) {
   CUtensorMap tm_w, tm_out;
   if (!make_row_maps(&tm_x, p.a, p.M, p.K, p.lda, 1) ||
       !make_grouped_map(&tm_w, p.b, p.G, p.N, p.K, p.K, 1, 128) ||
-      !make_store_map(&tm_out, p.out, 1, p.M, p.N, p.ldo, p.out_f32))
+      !make_store_map(&tm_out, p.out, 1, p.M, p.N, p.ldo, p.out_f32, 128))
     return cudaErrorInvalidValue;
   const long long tiles = (static_cast<long long>(p.M) / kTile + (p.M < p.G ? p.M : p.G)) * a.n_tiles;
   return launch_clusters<kern>(kThreads, 2, tiles, true, kSmemBytes, s, tm_x, tm_w, tm_out, a);
