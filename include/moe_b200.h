@@ -512,8 +512,8 @@ MOE_API int moe_dequantize_rows_fp8(const uint8_t* codes, const float* scales, i
  *   offsets [G + 1] int32 on the device, ascending, within [0, M]; rows before
  *   offsets[0] and from offsets[G] on belong to no group: they are not read
  *   into any result and the rows of y and dx there are left as they were.
- *   (Offsets are clamped to [0, M] and a group that ends before it starts is
- *   empty, so bad offsets give undefined results but no bad access.)
+ *   (Offsets are clamped to [0, M] and an offset below an earlier one counts
+ *   as that one, so bad offsets give no bad access.)
  *   NULL offsets with G = 1: one group of all rows.
  *   out_dtype: MOE_DTYPE_BF16 or MOE_DTYPE_FP32 (accumulate needs FP32).
  *   status: int32 device word that receives MOE_STATUS_WAIT_TIMEOUT | site if a

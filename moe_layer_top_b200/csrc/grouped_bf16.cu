@@ -102,7 +102,7 @@ __device__ __forceinline__ Tile tile_at(const Args& a, const int* off, const int
     r.n = C::kNTile;
     r.valid = min(C::kNTile, a.cols - r.n0);
     r.red0 = off[r.g];
-    r.red = max(0, off[r.g + 1] - r.red0);
+    r.red = off[r.g + 1] - r.red0;
   } else {
     r.g = group_of_tile(first, a.G, t);
     const int i = t - first[r.g];

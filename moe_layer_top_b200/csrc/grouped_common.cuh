@@ -388,42 +388,65 @@ __device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t smem_addr) {
   return d;
 }
 
-// Group tables in shared memory: off[g] (clamped to [0, M]: no access leaves
-// the tensors whatever the offsets hold) and, with `first`, the first tile of
-// each group, where a group has ceil(rows / row_tile) * per_row_tile tiles.
-// Returns their number.  All threads of the block take part; ends with a
-// block barrier.
+// Group tables in shared memory: off[g], the offsets clamped to [0, M] and made ascending (off[g] is the largest of
+// the first g + 1), so that no group leaves the tensors or takes another's rows whatever they hold; and, with
+// `first`, the first tile of each group, where a group has ceil(rows / row_tile) * per_row_tile tiles.  Returns their
+// number.  All threads of the block take part; ends with a block barrier.
 template <int kThreads>
 __device__ __forceinline__ int build_group_tables(const int32_t* offsets, int M, int G, int row_tile, int per_row_tile,
                                                   int* off, int* first, int* scan) {
-  for (int i = threadIdx.x; i <= G; i += kThreads) {
-    const int v = offsets ? offsets[i] : (i ? M : 0);
-    off[i] = v < 0 ? 0 : (v > M ? M : v);
+  static_assert(4 * kThreads >= kMaxGroups + 1 && kThreads / 32 <= 32, "four entries per thread");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (G == 1) {  // no scans on the way of a plain product
+    const int a = offsets ? min(max(offsets[0], 0), M) : 0;
+    const int b = offsets ? max(a, min(max(offsets[1], 0), M)) : M;
+    if (threadIdx.x == 0) {
+      off[0] = a;
+      off[1] = b;
+      if (first != nullptr) first[0] = 0;
+    }
+    __syncthreads();
+    return (b - a + row_tile - 1) / row_tile * per_row_tile;
+  }
+  // inclusive scan of a value per thread over the block: returns the value of the thread before (`none` for the first)
+  auto scan_before = [&](int v, int none, auto op) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v = op(v, u);
+    }
+    if (lane == 31) scan[warp] = v;
+    int before = __shfl_up_sync(0xffffffffu, v, 1);
+    if (lane == 0) before = none;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) before = op(before, scan[w]);
+    return before;
+  };
+  int o[4], top = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int g = 4 * threadIdx.x + j;
+    const int v = g > G ? 0 : (offsets ? offsets[g] : (g ? M : 0));
+    top = max(top, min(max(v, 0), M));
+    o[j] = top;
+  }
+  const int before = scan_before(top, 0, [](int x, int y) { return max(x, y); });
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int g = 4 * threadIdx.x + j;
+    if (g <= G) off[g] = max(o[j], before);
   }
   __syncthreads();
   if (first == nullptr) return 0;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int n[4], sum = 0;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int g = 4 * threadIdx.x + j;
     const int rows = g < G ? off[g + 1] - off[g] : 0;
-    n[j] = rows > 0 ? (rows + row_tile - 1) / row_tile * per_row_tile : 0;
+    n[j] = (rows + row_tile - 1) / row_tile * per_row_tile;
     sum += n[j];
   }
-  int incl = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
-  }
-  if (lane == 31) scan[warp] = incl;
-  __syncthreads();
-  int base = incl - sum, total = 0;
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) base += scan[w];
-    total += scan[w];
-  }
+  int base = scan_before(sum, 0, [](int x, int y) { return x + y; });
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int g = 4 * threadIdx.x + j;
@@ -431,6 +454,8 @@ __device__ __forceinline__ int build_group_tables(const int32_t* offsets, int M,
     base += n[j];
   }
   __syncthreads();
+  int total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) total += scan[w];
   return total;
 }
 

@@ -241,18 +241,19 @@ def test_gradients_against_differences():
         assert abs((loss(xd, wd + e) - loss(xd, wd - e)) / 2 - dw[i, n, k].double()) <= 1e-4
 
 
-def test_bad_offsets_stay_in_bounds():
-    """Offsets outside [0, M] and groups that end before they start give no access outside the tensors: the
-    bounds are clamped in the kernel, and the guard rows around the outputs stay."""
+@pytest.mark.parametrize("offs", [[-5, 20, 1000, 60], [40, 10, 30, 20], [2 ** 31 - 1, -2 ** 31, 50, 0], [7, 7, 3, 90]])
+def test_offsets_out_of_range_or_order(offs):
+    """They count as clamped to [0, M] and, where one is below an earlier one, as that one."""
     M, N, K = 50, 64, 128
-    x, w = _randn(26, M, K), _randn(27, 3, N, K)
+    x, w, dy = _randn(26, M, K), _randn(27, 3, N, K), _randn(28, M, N)
+    good = torch.tensor(offs, dtype=torch.int64).clamp(0, M).cummax(0).values.to(torch.int32).cuda()
+    off = torch.tensor(offs, dtype=torch.int32, device="cuda")
     guard = torch.full((M + 20, N), 7.0, dtype=torch.bfloat16, device="cuda")
-    for offs in ([-5, 20, 1000, 60], [40, 10, 30, 20], [2 ** 31 - 1, -2 ** 31, 50, 0]):
-        off = torch.tensor(offs, dtype=torch.int32, device="cuda")
-        ops.grouped_matmul(x, w, off, out=guard[10:10 + M])
-        ops.grouped_matmul_dw(_randn(28, M, N), x, off)
-        torch.cuda.synchronize()
-        assert (guard[:10] == 7).all() and (guard[10 + M:] == 7).all()
+    want = guard.clone()
+    ops.grouped_matmul(x, w, off, out=guard[10:10 + M])
+    ops.grouped_matmul(x, w, good, out=want[10:10 + M])
+    assert torch.equal(guard, want) and (guard[:10] == 7).all() and (guard[10 + M:] == 7).all()
+    assert torch.equal(ops.grouped_matmul_dw(dy, x, off), ops.grouped_matmul_dw(dy, x, good))
 
 
 def test_repeated_calls_agree_bit_for_bit():
