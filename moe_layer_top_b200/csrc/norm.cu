@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(V == 4 ? kMaxNormH / 32 : kMaxRowThreads, V ==
 // backward: a block walks rows (grid stride) and keeps its columns' weight
 // gradient in registers; each block writes one row of partial sums, which the
 // second kernel adds in block order, so the result does not depend on timing.
-// The next row's loads are in flight while a row's sum is formed.  Up to 512
+// The next row's loads are in flight while a row's sum is formed (V = 1).  Up to 512
 // columns a warp holds a row by itself and 16 of them share a block (then the
 // block adds their columns through shared memory first); otherwise the whole
 // block holds one row.
@@ -268,12 +268,17 @@ __global__ void __launch_bounds__(kMaxRowThreads) rms_norm_backward_kernel(const
   };
   const float inv_h = 1.0f / static_cast<float>(a.H);
   int buf = 0;
+  constexpr bool kAhead = V == 1;  // with two vectors per thread the copies do not fit the registers
   float next_rstd = 0.f;
-  if (first_row < a.T) {
+  if (kAhead && first_row < a.T) {
     load(first_row);
     next_rstd = a.rstd[first_row];
   }
   for (long long row = first_row; row < a.T; row += step) {
+    if (!kAhead) {
+      load(row);
+      next_rstd = a.rstd[row];
+    }
     const float rstd = next_rstd;
     f2 dots = both(0.f);
 #pragma unroll
@@ -294,7 +299,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) rms_norm_backward_kernel(const
       cs[i] = s[i];
       cr[i] = r[i];
     }
-    if (row + step < a.T) {
+    if (kAhead && row + step < a.T) {
       load(row + step);
       next_rstd = a.rstd[row + step];
     }
