@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (any) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) arrive_in_cluster(empty_bar + 8 * abuf);
+          if (elect_lane()) arrive_in_cluster(empty_bar + 8 * abuf);
         }
       } else {
         // a lane holds a row: 64 bytes of each go through shared memory as one TMA store of the warp's 32 rows
@@ -468,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (any) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) arrive_in_cluster(empty_bar + 8 * abuf);
+          if (elect_lane()) arrive_in_cluster(empty_bar + 8 * abuf);
         }
       }
       if (any) {

@@ -45,6 +45,7 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatil
 
 __device__ __forceinline__ bool warp_wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort, int* status,
                                               int where) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;  // the common case, without the bookkeeping
   const bool ok = wait_bar(bar, parity, abort, status, where);
   return __all_sync(0xffffffffu, ok);
 }

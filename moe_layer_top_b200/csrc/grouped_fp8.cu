@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 4; ++i) f[j * 128 + 32 * i] = xs[j][i] * ws[j];
         __syncwarp();
-        if (lane == 0) mbar_arrive(&factor_full[slot]);
+        if (elect_lane()) mbar_arrive(&factor_full[slot]);
         if (++slot == kBatches) {
           slot = 0;
           phase ^= 1u;
@@ -288,14 +288,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&acc_empty[abuf]);
+          if (elect_lane()) mbar_arrive(&acc_empty[abuf]);
           if (++abuf == kAccBufs) {
             abuf = 0;
             aphase ^= 1u;
           }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&factor_empty[slot]);
+        if (elect_lane()) mbar_arrive(&factor_empty[slot]);
         if (++slot == kBatches) {
           slot = 0;
           fphase ^= 1u;

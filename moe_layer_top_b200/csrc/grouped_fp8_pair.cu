@@ -26,7 +26,7 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 384;
-constexpr int kProducerRegs = 56, kEpilogueRegs = 224;  // 128 * 56 + 256 * 224 = 384 * 168, what the launch has
+constexpr int kProducerRegs = 88, kEpilogueRegs = 208;  // 128 * 88 + 256 * 208 = 384 * 168, what the launch has
 constexpr int kLaunchRegs = 168;
 // The scales' factors go through a ring of batches in shared memory: [column half][slot][K block][row].
 constexpr int kBatch = 4, kBatches = 3;
@@ -175,14 +175,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         for (int t = first_tile; t < num_tiles && ok; t += stride) {
           for (int kb = 0; kb < kb_n; ++kb) {
-            ok = warp_wait_bar(&acc_empty[abuf], aphase ^ 1u, abort_flag, args.status, kWhereGroupedMma) &&
-                 warp_wait_bar(&full[stage], phase, abort_flag, args.status, kWhereGroupedMma);
+            // (the operands are there long before the accumulator is: wait for that last)
+            const uint32_t d = tmem_base + static_cast<uint32_t>(abuf * kTile);
+            const uint32_t a = smem_u32(smem + static_cast<size_t>(stage) * kStageBytes);
+            const uint64_t ad = smem_desc_sw128(a), bd = smem_desc_sw128(a + 16384);
+            ok = warp_wait_bar(&full[stage], phase, abort_flag, args.status, kWhereGroupedMma) &&
+                 warp_wait_bar(&acc_empty[abuf], aphase ^ 1u, abort_flag, args.status, kWhereGroupedMma);
             if (!ok) break;
             tc_fence_after();
             if (elect_lane()) {
-              const uint32_t d = tmem_base + static_cast<uint32_t>(abuf * kTile);
-              const uint32_t a = smem_u32(smem + static_cast<size_t>(stage) * kStageBytes);
-              const uint64_t ad = smem_desc_sw128(a), bd = smem_desc_sw128(a + 16384);
 #pragma unroll
               for (int s = 0; s < 4; ++s) mma_fp8_for<true>(d, ad + 2 * s, bd + 2 * s, kIdesc, s > 0 ? 1u : 0u);
               commit_for<true>(&acc_full[abuf]);
@@ -237,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) f[j * 128 + 32 * i] = xs[j][i] * ws[j];
           __syncwarp();
-          if (lane == 0) mbar_arrive(&factor_full[g * kBatches + slot]);
+          if (elect_lane()) mbar_arrive(&factor_full[g * kBatches + slot]);
           if (++slot == kBatches) {
             slot = 0;
             phase ^= 1u;
@@ -276,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) f[j] = my_factors[(slot * kBatch + j) * 128];
         __syncwarp();
-        if (lane == 0) mbar_arrive(&factor_empty[g * kBatches + slot]);
+        if (elect_lane()) mbar_arrive(&factor_empty[g * kBatches + slot]);
         if (++slot == kBatches) {
           slot = 0;
           fphase ^= 1u;
@@ -302,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (c + 1 == kCols / kChunk) {
               tc_fence_before();
               __syncwarp();
-              if (lane == 0) arrive_in_cluster(empty_bar + 8 * abuf);
+              if (elect_lane()) arrive_in_cluster(empty_bar + 8 * abuf);
             }
             if (live) {
 #pragma unroll
