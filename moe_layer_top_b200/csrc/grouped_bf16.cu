@@ -32,6 +32,11 @@
 // Persistent (kSplit: one tile per cluster), 10 warps per CTA: TMA producer, MMA issuer (of the leader CTA),
 // eight epilogue warps; the accumulator is double-buffered in TMEM, so a
 // tile's stores run under the next tile's products.
+//
+// On a B200: 8192 x 4096 x 4096 forward and dx 177 us (1550 TFLOP/s, 0.94 of
+// the measured peak), dw 197 us; 32768 rows over 128 experts of 4096 x 1536
+// forward and dx 405 us, dw 510 us (bound by the power limit with HBM and the
+// tensor cores both busy); 512 rows over the same experts 244 us, 0.99 of HBM.
 #include "grouped_common.cuh"
 
 namespace moe {
@@ -69,7 +74,7 @@ struct Cfg {
   static constexpr bool kMnB = Kind == kGroupedDw;
   static constexpr int kTmemCols = 2 * kNTile;
   // dw: each epilogue warp stages boxes of 32 rows x 64 bytes for TMA stores (128 bytes would cost a stage of the
-  // ring, and the short reductions need them: dw of 32768 rows over 128 experts 526 us with five, 507 with six)
+  // ring, and the short reductions need them: dw of 32768 rows over 128 experts 525 us with five, 510 with six)
   static constexpr int kOutBytes = Kind == kGroupedDw && Mode != kModeSplit ? kGroupedEpiWarps * 2048 : 0;
   static constexpr int kStages = (kSmemMax - 1024 - kGroupedReserve - kOutBytes) / kStageBytes;
   static constexpr size_t kSmemBytes =
@@ -128,7 +133,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = Cfg<Kind, Mode>;
   constexpr bool kPair = C::kPair, kSplit = Mode == kModeSplit;
   // dw in a pair: a stage in which the group ends is counted, and cleared, by each CTA for itself, and the peer
-  // tells the leader when its half is ready (for every stage that would cost 28 of 258 us at 8192 x 4096 x 4096)
+  // tells the leader when its half is ready (that for every stage cost 11 % of 8192 x 4096 x 4096)
   constexpr bool kTails = kPair && Kind == kGroupedDw;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));

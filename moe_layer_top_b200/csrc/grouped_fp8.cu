@@ -13,7 +13,7 @@
 // of the group the N side, which comes in steps of 16: a tile of a few rows
 // costs the tensor core little (a 128 x 128 tile of 2 rows held the memory
 // stream back: 512 rows over 256 groups of 7168 x 2048 took 613 us that way,
-// 515 this way).  An epilogue thread holds one column of up to 64 rows; the
+// 500 this way).  An epilogue thread holds one column of up to 64 rows; the
 // rows' factors are read from shared memory, the same for all lanes.
 // kSplit: a cluster of up to eight CTAs shares the K blocks of one such tile,
 // each leaves its partial sums in shared memory and all add a part of them
@@ -379,12 +379,12 @@ cudaError_t launch_grouped_fp8(const GroupedProblem& p, cudaStream_t stream) {
   const long long single = row_tiles(p.M, p.G, 128) * ((p.N + 127) / 128);
   const int splits = choose_splits(single, p.num_sms, (p.K + 127) / 128);
   if (splits > 1) return launch_columns<true>(p, splits, stream);
-  // A pair takes 1.25 times as long for a K block of its 256 x 256 tile as a CTA for its 128 x 128 (0.6 against
-  // 0.48 us), so it wins unless the larger tiles leave SMs idle or rows empty: N = 4096, K = 7168: 512 rows 31 us
-  // in single tiles, 37 in pairs; 1024 rows 57 and 38 us.
+  // A pair computes its 256 x 256 tile in the time that a CTA takes for 128 x 128, so it wins unless the larger tiles
+  // leave SMs idle (N = 4096, K = 7168: 512 rows 32 us in pairs and 34 in single tiles, 1024 rows 33 and 64 us) or
+  // most of their rows empty: single tiles fit a group's rows in steps of 16.
   const int sms = p.num_sms, pairs = p.num_sms / 2;
   const long long pair = row_tiles(p.M, p.G, 256) * ((p.N + 255) / 256);
-  const bool use_pair = 5 * ((pair + pairs - 1) / pairs) <= 4 * ((single + sms - 1) / sms);
+  const bool use_pair = p.M / p.G > 128 && (pair + pairs - 1) / pairs <= (single + sms - 1) / sms;
   return use_pair ? launch_grouped_fp8_pair(p, stream) : launch_columns<false>(p, 1, stream);
 }
 

@@ -12,7 +12,10 @@
 // reads that sum, differentiates the function that ran.  Codes are those of
 // the rounded y, so they equal what quantising y afterwards would give.  All
 // sums are fp32.  Everything here is bound by HBM: one pass, the row stays in
-// registers between the sum and the output, 16 bytes per access.
+// registers between the sum and the output, 16 bytes per access.  On a B200
+// (6551 GB/s of copy): 8192 x 7168 with residual and FP8 output 63 us, 0.99 of
+// the copy rate; backward of 16384 x 4096 with a residual gradient 86 us, 0.96;
+// quantising 8192 x 7168 34 us, 0.79; reading it back 29 us, 0.94.
 #include "common.cuh"
 #include "kernels.h"
 #include "rows.h"
@@ -147,11 +150,9 @@ __device__ __forceinline__ uint2 quantize8(const uint4& u, float* scale_out) {
 // ----------------------------------------------------------------------------
 // forward: blockDim.x threads per row (a multiple of 32), V vectors of 8
 // columns each; blockDim.y rows per block when one warp covers a row.
-// (V = 4 is held to 64 registers: with the 85 that it would take, half as many
-// rows are in flight and 8192 x 7168 takes 100 us instead of 73.)
 // ----------------------------------------------------------------------------
 template <int V>
-__global__ void __launch_bounds__(V == 4 ? kMaxNormH / 32 : kMaxRowThreads, V == 4 ? 2 : 1) rms_norm_kernel(const RmsNormArgs a) {
+__global__ void __launch_bounds__(V == 4 ? kMaxNormH / 32 : kMaxRowThreads) rms_norm_kernel(const RmsNormArgs a) {
   pdl_launch_dependents();
   pdl_wait();
   __shared__ float sums[32];
@@ -444,7 +445,7 @@ int row_threads(int vecs, int v) { return ((vecs + v - 1) / v + 31) / 32 * 32; }
 cudaError_t launch_rms_norm(const RmsNormArgs& a, cudaStream_t stream) {
   const int vecs = a.H / 8;
   // Few rows: a thread per vector, the shortest way through one row.  Many: up to four vectors per thread, so that
-  // an SM has more rows in flight (T = 8192, H = 7168, residual and FP8 output: 101 us with one, 73 us with four).
+  // an SM has more rows in flight (T = 8192, H = 7168, residual and FP8 output: 88 us with one, 63 us with four).
   const int v = a.T <= 2 * 148 ? (vecs > 1024 ? 2 : 1) : (vecs > 64 ? 4 : (vecs > 32 ? 2 : 1));
   const int tx = row_threads(vecs, v);
   const int ty = tx == 32 ? 8 : 1;
@@ -501,7 +502,7 @@ cudaError_t launch_rms_norm_backward(const RmsNormBackwardArgs& a, float* dweigh
 cudaError_t launch_quantize_rows(const void* x, long long ldx, long long rows, int cols, uint8_t* codes,
                                  float* scales, cudaStream_t stream) {
   const int groups = (cols + 127) / 128;
-  // four groups per half-warp where there is work for every SM (8192 x 7168: 52 us with one, 45 us with four)
+  // four groups per half-warp where there is work for every SM (8192 x 7168: 44 us with one, 34 us with four)
   const int items = rows * groups >= 148 * 8 * 64 ? 4 : 1;
   const int block_rows = groups < items * 16 ? items * 16 / groups : 1;
   const long long blocks = block_rows > 1 ? (rows + block_rows - 1) / block_rows
