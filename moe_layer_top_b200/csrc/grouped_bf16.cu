@@ -195,7 +195,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------------ producer (of each CTA)
-    const uint64_t pol = policy_evict_normal();
+    // dw: the rows are read again by every tile of their group, the gradient passing by is not read (8192 x 4096 x
+    // 4096: 194 us, 199 without the hint; on the weights or rows of the other two it costs up to 5 %)
+    const uint64_t pol = Kind == kGroupedDw ? policy_evict_last() : policy_evict_normal();
     int stage = 0;
     uint32_t phase = 0;
     long long fills = 0;

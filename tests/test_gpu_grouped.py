@@ -177,6 +177,26 @@ def test_dense_fp8_takes_the_layers_quantised_weights():
     assert_within(y, xv @ wv.t(), product_bound(xv @ wv.t(), xv.abs() @ wv.abs().t(), K, torch.float32, fp8=True))
 
 
+@pytest.mark.parametrize("sizes,N,K", [([5, 3, 140], 264, 272), LARGE[0]])
+def test_fp8_rows_with_nan_stay_their_own(sizes, N, K):
+    """A NaN code spoils its own row; a NaN in a group's weights only that group's column."""
+    off = offsets_of(sizes)
+    M = int(off[-1])
+    codes, scales = quantize_rows(_randn(33, M, K))
+    w, ws = quantize_weight(_randn(34, len(sizes), N, K, std=0.1))
+    clean = ops.grouped_matmul(codes, w, off, x_scale=scales, w_scale=ws)
+    bad_rows = [0, int(off[-1]) - 1, int(off[1])]
+    for r in bad_rows:
+        codes[r, r % K] = 0x7F
+    w[-1, 9, 7] = 0xFF
+    got = ops.grouped_matmul(codes, w, off, x_scale=scales, w_scale=ws)
+    want = clean.clone()
+    want[bad_rows] = float("nan")
+    want[int(off[-2]):, 9] = float("nan")
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    assert torch.equal(got[~torch.isnan(got)], clean[~torch.isnan(got)])
+
+
 def test_one_group_without_offsets():
     x, w = _randn(16, 200, 256), _randn(17, 1, 136, 256, std=0.1)
     y = ops.grouped_matmul(x, w, None)
