@@ -465,7 +465,8 @@ MOE_API int moe_combine_reduce_scatter_emulated(int32_t T, int32_t topk, int32_t
  *   (receives r, for the backward pass): each may be NULL.
  * H is a multiple of 8 up to 16384 (of 16 with codes).  residual_out may be
  * residual or x, y may be any of the inputs [T, H] that residual_out is not.
- * Sums are fp32: a row whose squares add up to more than fp32 holds gives 0.
+ * Sums are fp32: a row whose squares add up to more than fp32 holds gives 0
+ * (and a row of zeros with eps = 0 gives NaN).
  */
 MOE_API int moe_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr, void* residual_out,
                          int64_t ldo, const void* weight, float eps, int32_t T, int32_t H, void* y, int64_t ldy,

@@ -16,6 +16,7 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 
 int cuda_result(cudaError_t e, const char* what) {
   if (e == cudaSuccess) return MOE_OK;
+  cudaGetLastError();  // reported here; not left behind for another caller's check
   return api_fail(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 

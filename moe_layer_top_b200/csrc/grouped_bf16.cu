@@ -12,7 +12,7 @@
 //
 // forward, dx: the weight fills the MMA's M side and the group's rows its N
 // side, because N comes in steps of 16 or 32 and M only whole: a group's rows
-// are cut into equal tiles of at most kRowTile, each rounded up by less than a
+// are cut into equal tiles of at most 256 (128), each rounded up by less than a
 // step, so a ragged group wastes little and one row costs little more than
 // its weights.  A tile that runs past its group's end computes rows of the
 // next group and does not store them.
@@ -29,9 +29,10 @@
 // tile, each leaves its partial sums in shared memory and all add a part of
 // them up, in rank order: where tiles are few, all SMs stream operands.
 //
-// Persistent (kSplit: one tile per cluster), 10 warps per CTA: TMA producer, MMA issuer (of the leader CTA),
-// eight epilogue warps; the accumulator is double-buffered in TMEM, so a
-// tile's stores run under the next tile's products.
+// Persistent (kSplit: one tile per cluster), 10 warps per CTA: TMA producer,
+// MMA issuer (of the leader CTA), eight epilogue warps; the accumulator is
+// double-buffered in TMEM, so a tile's stores run under the next tile's
+// products.
 //
 // On a B200: 8192 x 4096 x 4096 forward and dx 177 us (1550 TFLOP/s, 0.94 of
 // the measured peak), dw 197 us; 32768 rows over 128 experts of 4096 x 1536
