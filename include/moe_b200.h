@@ -519,8 +519,8 @@ MOE_API int moe_dequantize_rows_fp8(const uint8_t* codes, const float* scales, i
  *   out_dtype: MOE_DTYPE_BF16 or MOE_DTYPE_FP32 (accumulate needs FP32).
  *   status: int32 device word that receives MOE_STATUS_WAIT_TIMEOUT | site if a
  *   bounded in-kernel wait runs out (never cleared here), or NULL.
- * 1 <= G <= 1024; N and K are multiples of 8 (FP8: K of 16).  Accumulation is
- * fp32 and each result is rounded once; results do not depend on timing.
+ * 1 <= G <= 1024; M, N and K up to 2^30, N and K multiples of 8 (FP8: K of 16).
+ * Accumulation is fp32 and each result is rounded once; results do not depend on timing.
  * The outputs must not overlap the inputs.
  */
 MOE_API int moe_grouped_matmul(const void* x, int64_t ldx, const void* w, const int32_t* offsets, int32_t M,

@@ -43,15 +43,20 @@ int check_norm_shape(const char* what, int32_t T, int32_t H) {
   return MOE_OK;
 }
 
-// Sizes common to the matrix products.
-int check_product(const char* what, int32_t M, int32_t G, int32_t N, int32_t K, bool fp8, const int32_t* offsets) {
+// Sizes common to the matrix products.  (The kernels round positions up to their tiles in 32 bits: hence 2^30.)
+int check_product(const char* what, int32_t M, int32_t G, int32_t N, int32_t K, bool fp8, const int32_t* offsets,
+                  const int32_t* status) {
+  constexpr int32_t kMost = 1 << 30;
   if (M < 0) return api_fail(MOE_ERR_INVALID, "%s: M = %d < 0", what, M);
+  if (M > kMost || N > kMost || K > kMost)
+    return api_fail(MOE_ERR_INVALID, "%s: M = %d, N = %d or K = %d above 2^30", what, M, N, K);
   if (G < 1 || G > 1024) return api_fail(MOE_ERR_INVALID, "%s: G = %d outside [1, 1024]", what, G);
   if (N <= 0 || N % 8) return api_fail(MOE_ERR_INVALID, "%s: N = %d is not a positive multiple of 8", what, N);
   if (K <= 0 || K % (fp8 ? 16 : 8))
     return api_fail(MOE_ERR_INVALID, "%s: K = %d is not a positive multiple of %d", what, K, fp8 ? 16 : 8);
   if (!offsets && G != 1) return api_fail(MOE_ERR_INVALID, "%s: offsets may be NULL for one group only (G = %d)", what, G);
   if (!aligned(offsets, 4)) return api_fail(MOE_ERR_INVALID, "%s: offsets is not 4-byte aligned", what);
+  if (!aligned(status, 4)) return api_fail(MOE_ERR_INVALID, "%s: status is not 4-byte aligned", what);
   const int64_t tiles = (static_cast<int64_t>(M) / 128 + G) * ((static_cast<int64_t>(N > K ? N : K) + 127) / 128);
   const int64_t dw_tiles = static_cast<int64_t>(G) * ((N + 127) / 128) * ((K + 127) / 128);
   if (tiles >= (int64_t(1) << 30) || dw_tiles >= (int64_t(1) << 30))
@@ -73,7 +78,7 @@ int run_product(moe::GroupedProblem& p, const char* what, void* stream) {
 int matmul_fp8(const char* what, const uint8_t* x, const float* x_scale, const uint8_t* w, const float* w_scale,
                const int32_t* offsets, int32_t M, int32_t G, int32_t N, int32_t K, void* y, int64_t ldy,
                int32_t out_dtype, int32_t* status, void* stream) {
-  MOE_TRY(check_product(what, M, G, N, K, true, offsets));
+  MOE_TRY(check_product(what, M, G, N, K, true, offsets, status));
   MOE_TRY(check_out_dtype(what, out_dtype));
   if (M == 0) return MOE_OK;
   const int out_bytes = out_dtype == MOE_DTYPE_FP32 ? 4 : 2;
@@ -221,7 +226,7 @@ int moe_grouped_matmul_fp8(const uint8_t* x, const float* x_scale, const uint8_t
 int moe_grouped_matmul(const void* x, int64_t ldx, const void* w, const int32_t* offsets, int32_t M, int32_t G,
                        int32_t N, int32_t K, void* y, int64_t ldy, int32_t out_dtype, int32_t* status, void* stream) {
   const char* what = "grouped_matmul";
-  MOE_TRY(check_product(what, M, G, N, K, false, offsets));
+  MOE_TRY(check_product(what, M, G, N, K, false, offsets, status));
   MOE_TRY(check_out_dtype(what, out_dtype));
   if (M == 0) return MOE_OK;
   MOE_TRY(check_rows(what, "x", x, ldx, K, 2));
@@ -243,7 +248,7 @@ int moe_grouped_matmul_dx(const void* dy, int64_t lddy, const void* w, const int
                           int32_t N, int32_t K, void* dx, int64_t lddx, int32_t out_dtype, int32_t* status,
                           void* stream) {
   const char* what = "grouped_matmul_dx";
-  MOE_TRY(check_product(what, M, G, N, K, false, offsets));
+  MOE_TRY(check_product(what, M, G, N, K, false, offsets, status));
   MOE_TRY(check_out_dtype(what, out_dtype));
   if (M == 0) return MOE_OK;
   MOE_TRY(check_rows(what, "dy", dy, lddy, N, 2));
@@ -265,7 +270,7 @@ int moe_grouped_matmul_dw(const void* dy, int64_t lddy, const void* x, int64_t l
                           int32_t G, int32_t N, int32_t K, void* dw, int32_t out_dtype, int32_t accumulate,
                           int32_t* status, void* stream) {
   const char* what = "grouped_matmul_dw";
-  MOE_TRY(check_product(what, M, G, N, K, false, offsets));
+  MOE_TRY(check_product(what, M, G, N, K, false, offsets, status));
   MOE_TRY(check_out_dtype(what, out_dtype));
   if (accumulate != 0 && accumulate != 1) return api_fail(MOE_ERR_INVALID, "%s: accumulate must be 0 or 1", what);
   if (accumulate && out_dtype != MOE_DTYPE_FP32)

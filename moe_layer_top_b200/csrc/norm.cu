@@ -487,7 +487,7 @@ int rms_norm_backward_blocks(int T, int H) {
   const BackwardShape b = backward_shape(H);
   const int threads = b.tx * b.ty;
   const int most = threads >= 512 ? 2 * 148 : 148 * (1024 / threads > 8 ? 8 : 1024 / threads);
-  const int want = (T + b.ty - 1) / b.ty;
+  const int want = T / b.ty + (T % b.ty != 0);
   return want < most ? want : most;
 }
 

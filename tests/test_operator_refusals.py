@@ -102,6 +102,24 @@ def test_grouped_products(L, kw, code):
                                    None) == code
 
 
+@pytest.mark.parametrize("kw", [dict(M=2 ** 30 + 1, N=8, K=8), dict(M=2 ** 31 - 1, N=8, K=8), dict(M=8, N=2 ** 30 + 8, K=8),
+                                dict(M=8, N=8, K=2 ** 31 - 8), dict(M=8, N=8, K=8, status=BYTE)])
+def test_products_whose_positions_leave_32_bits(L, kw):
+    a = {"status": None, **kw}
+    ld, sizes = 2 ** 31, (a["M"], 1, a["N"], a["K"])
+    tail = (G, ld, 0, a["status"], None)
+    assert L.moe_grouped_matmul(G, ld, G, G, *sizes, *tail) == ops.MOE_ERR_INVALID
+    assert L.moe_grouped_matmul_dx(G, ld, G, G, *sizes, *tail) == ops.MOE_ERR_INVALID
+    assert L.moe_grouped_matmul_dw(G, ld, G, ld, G, *sizes, G, 0, 0, a["status"], None) == ops.MOE_ERR_INVALID
+    k = max(a["K"] // 16 * 16, 16)
+    assert L.moe_matmul_fp8(G, G, G, G, a["M"], a["N"], k, *tail) == ops.MOE_ERR_INVALID
+
+
+def test_backward_workspace_of_the_most_rows(L):
+    most = L.moe_rms_norm_backward_workspace_size(1 << 24, 8)
+    assert L.moe_rms_norm_backward_workspace_size(2 ** 31 - 1, 8) == most > 0
+
+
 def test_accumulated_gradient_needs_fp32(L):
     args = (G, 256, G, 256, G, 10, 4, 256, 256, G)
     assert L.moe_grouped_matmul_dw(*args, ops.DTYPE_BF16, 1, None, None) == ops.MOE_ERR_UNSUPPORTED
