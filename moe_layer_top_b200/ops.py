@@ -414,7 +414,7 @@ def combine_reduce_scatter_emulated(T, topk, H, ranks, epoch, timeout_us=2_000_0
 # ----------------------------------------------------------------------------- stand-alone operators
 # Tensors of other types, shapes, devices or layouts than a function documents raise ValueError here; what
 # the C ABI checks (sizes, alignment) raises MoeError.  The work runs on `stream`, or on the current stream
-# of the tensors' device.
+# of the tensors' device; outputs and workspaces are allocated for that stream.
 _OUT_DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_FP32}
 
 
@@ -459,14 +459,24 @@ def _sizes(name, t, dims=2):
     return t.shape
 
 
-def _run(fn, device, stream, *args):
+def _on(stream, t):
+    """The context of a call that was given a stream: what it allocates belongs to that stream, so that neither a
+    workspace that it drops nor an output that its caller drops is handed out while the stream still uses it."""
+    if not isinstance(stream, torch.cuda.Stream):
+        raise ValueError(f"stream: a torch.cuda.Stream is needed, got {type(stream).__name__}")
+    if isinstance(t, torch.Tensor) and t.is_cuda and stream.device != t.device:
+        raise ValueError(f"stream: on {stream.device}, needed on the device of the first argument ({t.device})")
+    return torch.cuda.stream(stream)
+
+
+def _run(fn, device, *args):
     """Call a C entry point on the tensors' device, whichever device is current.  (These calls are as short as
     their kernels: addresses go as plain numbers and the stream is read as one.)"""
     index = device.index
     if index != torch._C._cuda_getDevice():
         with torch.cuda.device(device):
-            return _run(fn, device, stream, *args)
-    rc = fn(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
+            return _run(fn, device, *args)
+    rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     if rc:
         _check(rc)
 
@@ -476,11 +486,16 @@ def _like(x, dtype=None):
     return torch.empty_like(x, dtype=dtype, memory_format=torch.contiguous_format)
 
 
-def _out(out, out_dtype, rows, cols, like):
-    """The output of a product, new or checked: (tensor, address, elements between rows, type's number)."""
-    dtype = out_dtype or (torch.bfloat16 if out is None else out.dtype)
+def _out_dtype(out, out_dtype):
+    dtype = out_dtype or (torch.bfloat16 if out is None else getattr(out, "dtype", None))
     if dtype not in _OUT_DTYPES:
         raise ValueError(f"out_dtype: {dtype}, torch.bfloat16 or torch.float32 is needed")
+    return dtype
+
+
+def _out(out, out_dtype, rows, cols, like):
+    """The output of a product, new or checked: (tensor, address, elements between rows, type's number)."""
+    dtype = _out_dtype(out, out_dtype)
     if out is None:
         out = torch.empty(rows, cols, dtype=dtype, device=like.device)
         return out, out.data_ptr(), cols, _OUT_DTYPES[dtype]
@@ -507,6 +522,9 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, *, residu
     residual itself; None without residual), ``y`` (bf16 [T, H]; True allocates it, a tensor receives it, False
     leaves it out), ``codes`` and ``scales`` (with ``fp8``: the FP8 rows of y, uint8 [T, H] and fp32
     [ceil(H / 128), T]) and ``rstd`` (fp32 [T] if asked for)."""
+    if stream is not None:
+        with _on(stream, x):
+            return rms_norm(x, weight, eps, residual=residual, residual_out=residual_out, y=y, fp8=fp8, rstd=rstd)
     shape = T, H = _sizes("x", x)
     dev, bf16 = x.device, torch.bfloat16
     x_p, x_ld = _rows("x", x, bf16, shape, dev)
@@ -535,7 +553,7 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, *, residu
     if rstd:
         rstd = x.new_empty(T, dtype=torch.float32)
         rstd_p = rstd.data_ptr()
-    _run(lib().moe_rms_norm, dev, stream, x_p, x_ld, r_p, r_ld or 0, o_p, o_ld or 0, w_p, eps, T, H, y_p, y_ld or 0,
+    _run(lib().moe_rms_norm, dev, x_p, x_ld, r_p, r_ld or 0, o_p, o_ld or 0, w_p, eps, T, H, y_p, y_ld or 0,
          c_p, s_p, rstd_p)
     return {"residual": residual_out, "y": y, "codes": codes, "scales": scales,
             "rstd": rstd if rstd_p is not None else None}
@@ -548,6 +566,9 @@ def rms_norm_backward(dy: torch.Tensor, s: torch.Tensor, weight: torch.Tensor, r
     ``s`` is what was normalised (x, or the ``residual`` that the forward pass returned), ``dresidual`` the
     gradient that reaches it by other ways; ``ws`` a uint8 workspace of
     ``moe_rms_norm_backward_workspace_size`` bytes (allocated if not given)."""
+    if stream is not None:
+        with _on(stream, dy):
+            return rms_norm_backward(dy, s, weight, rstd, dresidual=dresidual, dx=dx, ws=ws)
     shape = T, H = _sizes("dy", dy)
     dev, bf16 = dy.device, torch.bfloat16
     dy_p, dy_ld = _rows("dy", dy, bf16, shape, dev)
@@ -565,25 +586,31 @@ def rms_norm_backward(dy: torch.Tensor, s: torch.Tensor, weight: torch.Tensor, r
     if ws is None:
         ws = dy.new_empty(max(L.moe_rms_norm_backward_workspace_size(T, H), 16), dtype=torch.uint8)
     else:
-        _flat("ws", ws, torch.uint8, ws.shape, dev)
-    _run(L.moe_rms_norm_backward, dev, stream, dy_p, dy_ld, s_p, s_ld, w_p, rstd_p, r_p, r_ld, T, H, dx_p, dx_ld,
+        _flat("ws", ws, torch.uint8, getattr(ws, "shape", None), dev)
+    _run(L.moe_rms_norm_backward, dev, dy_p, dy_ld, s_p, s_ld, w_p, rstd_p, r_p, r_ld, T, H, dx_p, dx_ld,
          dweight.data_ptr(), ws.data_ptr(), ws.numel())
     return dx, dweight
 
 
 def quantize_rows_fp8(x: torch.Tensor, stream=None):
     """bf16 [rows, cols] -> FP8 rows: (E4M3 codes as uint8 [rows, cols], fp32 scales [ceil(cols / 128), rows])."""
+    if stream is not None:
+        with _on(stream, x):
+            return quantize_rows_fp8(x)
     shape = rows, cols = _sizes("x", x)
     dev = x.device
     x_p, x_ld = _rows("x", x, torch.bfloat16, shape, dev)
     codes = _like(x, torch.uint8)
     scales = torch.empty((cols + 127) // 128, rows, dtype=torch.float32, device=dev)
-    _run(lib().moe_quantize_rows_fp8, dev, stream, x_p, x_ld, rows, cols, codes.data_ptr(), scales.data_ptr())
+    _run(lib().moe_quantize_rows_fp8, dev, x_p, x_ld, rows, cols, codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
 
 def dequantize_rows_fp8(codes: torch.Tensor, scales: torch.Tensor, *, out=None, stream=None):
     """FP8 rows -> the bf16 [rows, cols] values that they stand for."""
+    if stream is not None:
+        with _on(stream, codes):
+            return dequantize_rows_fp8(codes, scales, out=out)
     shape = rows, cols = _sizes("codes", codes)
     dev = codes.device
     c_p = _flat("codes", codes, torch.uint8, shape, dev)
@@ -593,7 +620,7 @@ def dequantize_rows_fp8(codes: torch.Tensor, scales: torch.Tensor, *, out=None, 
         o_p, o_ld = out.data_ptr(), cols
     else:
         o_p, o_ld = _rows("out", out, torch.bfloat16, shape, dev)
-    _run(lib().moe_dequantize_rows_fp8, dev, stream, c_p, s_p, rows, cols, o_p, o_ld)
+    _run(lib().moe_dequantize_rows_fp8, dev, c_p, s_p, rows, cols, o_p, o_ld)
     return out
 
 
@@ -601,6 +628,9 @@ def matmul_fp8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale:
                out_dtype=None, status=None, stream=None):
     """y [M, N] = x . w^T of FP8 rows x [M, K] (codes and scales of :func:`quantize_rows_fp8` or
     :func:`rms_norm`) and a weight w [N, K] with one scale per 128 x 128 block; bf16 or fp32."""
+    if stream is not None:
+        with _on(stream, x):
+            return matmul_fp8(x, x_scale, w, w_scale, out=out, out_dtype=out_dtype, status=status)
     M, K = _sizes("x", x)
     N = _sizes("w", w)[0]
     dev, kb = x.device, (K + 127) // 128
@@ -609,7 +639,7 @@ def matmul_fp8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale:
     w_p = _flat("w", w, torch.uint8, (N, K), dev)
     ws_p = _flat("w_scale", w_scale, torch.float32, ((N + 127) // 128, kb), dev)
     out, o_p, o_ld, dtype = _out(out, out_dtype, M, N, x)
-    _run(lib().moe_matmul_fp8, dev, stream, x_p, xs_p, w_p, ws_p, M, N, K, o_p, o_ld, dtype, _status(status, dev))
+    _run(lib().moe_matmul_fp8, dev, x_p, xs_p, w_p, ws_p, M, N, K, o_p, o_ld, dtype, _status(status, dev))
     return out
 
 
@@ -620,6 +650,10 @@ def grouped_matmul(x: torch.Tensor, w: torch.Tensor, offsets, *, x_scale=None, w
     x [M, K] bf16 and w [G, N, K] bf16; or FP8 rows x with ``x_scale`` [ceil(K / 128), M] and E4M3 weights with
     ``w_scale`` [G, ceil(N / 128), ceil(K / 128)].  ``offsets`` int32 [G + 1] on the device (None: one group of
     all rows).  y [M, N] bf16 or fp32; rows of no group are not written."""
+    if stream is not None:
+        with _on(stream, x):
+            return grouped_matmul(x, w, offsets, x_scale=x_scale, w_scale=w_scale, out=out, out_dtype=out_dtype,
+                                  status=status)
     M, K = _sizes("x", x)
     G, N, _ = _sizes("w", w, 3)
     dev = x.device
@@ -630,7 +664,7 @@ def grouped_matmul(x: torch.Tensor, w: torch.Tensor, offsets, *, x_scale=None, w
         x_p, x_ld = _rows("x", x, torch.bfloat16, (M, K), dev)
         w_p = _flat("w", w, torch.bfloat16, (G, N, K), dev)
         out, o_p, o_ld, dtype = _out(out, out_dtype, M, N, x)
-        _run(lib().moe_grouped_matmul, dev, stream, x_p, x_ld, w_p, off_p, M, G, N, K, o_p, o_ld, dtype,
+        _run(lib().moe_grouped_matmul, dev, x_p, x_ld, w_p, off_p, M, G, N, K, o_p, o_ld, dtype,
              _status(status, dev))
         return out
     kb = (K + 127) // 128
@@ -639,7 +673,7 @@ def grouped_matmul(x: torch.Tensor, w: torch.Tensor, offsets, *, x_scale=None, w
     xs_p = _flat("x_scale", x_scale, torch.float32, (kb, M), dev)
     ws_p = _flat("w_scale", w_scale, torch.float32, (G, (N + 127) // 128, kb), dev)
     out, o_p, o_ld, dtype = _out(out, out_dtype, M, N, x)
-    _run(lib().moe_grouped_matmul_fp8, dev, stream, x_p, xs_p, w_p, ws_p, off_p, M, G, N, K, o_p, o_ld, dtype,
+    _run(lib().moe_grouped_matmul_fp8, dev, x_p, xs_p, w_p, ws_p, off_p, M, G, N, K, o_p, o_ld, dtype,
          _status(status, dev))
     return out
 
@@ -647,6 +681,9 @@ def grouped_matmul(x: torch.Tensor, w: torch.Tensor, offsets, *, x_scale=None, w
 def grouped_matmul_dx(dy: torch.Tensor, w: torch.Tensor, offsets, *, out=None, out_dtype=None, status=None,
                       stream=None):
     """Gradient of :func:`grouped_matmul`'s rows: dx[r] = dy[r] . w[g] (dy [M, N], w [G, N, K] bf16 -> [M, K])."""
+    if stream is not None:
+        with _on(stream, dy):
+            return grouped_matmul_dx(dy, w, offsets, out=out, out_dtype=out_dtype, status=status)
     M, N = _sizes("dy", dy)
     G, _, K = _sizes("w", w, 3)
     dev = dy.device
@@ -654,7 +691,7 @@ def grouped_matmul_dx(dy: torch.Tensor, w: torch.Tensor, offsets, *, out=None, o
     w_p = _flat("w", w, torch.bfloat16, (G, N, K), dev)
     off_p = _offsets(offsets, G, dev)
     out, o_p, o_ld, dtype = _out(out, out_dtype, M, K, dy)
-    _run(lib().moe_grouped_matmul_dx, dev, stream, dy_p, dy_ld, w_p, off_p, M, G, N, K, o_p, o_ld, dtype,
+    _run(lib().moe_grouped_matmul_dx, dev, dy_p, dy_ld, w_p, off_p, M, G, N, K, o_p, o_ld, dtype,
          _status(status, dev))
     return out
 
@@ -663,23 +700,24 @@ def grouped_matmul_dw(dy: torch.Tensor, x: torch.Tensor, offsets, *, out=None, o
                       status=None, stream=None):
     """Gradient of :func:`grouped_matmul`'s weights: dw[g] = sum of dy[r]^T x[r] over the group's rows (dy [M, N],
     x [M, K] bf16 -> [G, N, K] bf16 or fp32; zero for an empty group).  ``accumulate`` adds to an fp32 ``out``."""
+    if stream is not None:
+        with _on(stream, dy):
+            return grouped_matmul_dw(dy, x, offsets, out=out, out_dtype=out_dtype, accumulate=accumulate, status=status)
     M, N = _sizes("dy", dy)
     K = _sizes("x", x)[1]
     dev = dy.device
     dy_p, dy_ld = _rows("dy", dy, torch.bfloat16, (M, N), dev)
     x_p, x_ld = _rows("x", x, torch.bfloat16, (M, K), dev)
-    G = 1 if offsets is None else offsets.numel() - 1
+    G = 1 if offsets is None else _sizes("offsets", offsets, 1)[0] - 1
     off_p = _offsets(offsets, G, dev)
     if accumulate and out is None:
         raise ValueError("accumulate: needs out")
-    dtype = out_dtype or (torch.bfloat16 if out is None else out.dtype)
-    if dtype not in _OUT_DTYPES:
-        raise ValueError(f"out_dtype: {dtype}, torch.bfloat16 or torch.float32 is needed")
+    dtype = _out_dtype(out, out_dtype)
     if out is None:
         out = torch.empty(G, N, K, dtype=dtype, device=dev)
         o_p = out.data_ptr()
     else:
         o_p = _flat("out", out, dtype, (G, N, K), dev)
-    _run(lib().moe_grouped_matmul_dw, dev, stream, dy_p, dy_ld, x_p, x_ld, off_p, M, G, N, K, o_p, _OUT_DTYPES[dtype],
+    _run(lib().moe_grouped_matmul_dw, dev, dy_p, dy_ld, x_p, x_ld, off_p, M, G, N, K, o_p, _OUT_DTYPES[dtype],
          1 if accumulate else 0, _status(status, dev))
     return out

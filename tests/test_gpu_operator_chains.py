@@ -185,6 +185,28 @@ def test_the_stream_argument():
     assert torch.equal(out, want) and torch.equal(y, ops.rms_norm(t["x"], t["gain"], EPS)["y"])
 
 
+def test_outputs_belong_to_the_stream_argument():
+    """Memory that the current stream has freed but has still to write is not handed to a call on another stream."""
+    x, dy = _randn(75, 512, 4096), _randn(76, 512, 4096)
+    gain = (1 + 0.1 * _randn(77, 4096)).to(torch.bfloat16)
+    w = _randn(78, 1, 4096, 4096)
+    rstd = ops.rms_norm(x, gain, EPS, rstd=True)["rstd"]
+    s = torch.cuda.Stream()
+    calls = [lambda **kw: ops.rms_norm_backward(dy, x, gain, rstd, **kw)[0],
+             lambda **kw: ops.rms_norm(x, gain, EPS, **kw)["y"],
+             lambda **kw: ops.grouped_matmul(x, w, None, **kw)]
+    for call in calls:
+        want = call()
+        late = torch.empty_like(want)
+        torch.cuda.synchronize()
+        torch.cuda._sleep(50_000_000)  # about 25 ms
+        late.fill_(float("nan"))
+        del late
+        got = call(stream=s)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+
+
 def test_another_device_than_the_current_one():
     if torch.cuda.device_count() < 2:
         pytest.skip("one device")

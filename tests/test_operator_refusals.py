@@ -159,6 +159,8 @@ def _cpu(*shape, dtype=torch.bfloat16):
     lambda: ops.grouped_matmul_dx(_cpu(4, 8), _cpu(2, 8, 64), None),
     lambda: ops.grouped_matmul_dw(_cpu(4, 8), _cpu(4, 64), None),
     lambda: ops.rms_norm("x", _cpu(64)),
+    lambda: ops.rms_norm(_cpu(4, 64), _cpu(64), stream=0),
+    lambda: ops.quantize_rows_fp8(_cpu(4, 64), 7),
 ])
 def test_python_refuses_other_tensors(call):
     with pytest.raises(ValueError):
