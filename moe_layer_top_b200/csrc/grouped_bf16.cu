@@ -202,6 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int stage = 0;
     uint32_t phase = 0;
     long long fills = 0;
+    uint32_t tails = 0, tail_odd = 0;  // kTails: stages with tails of the peer's own, and the parity of their number
     bool ok = true;
     for (int t = first_tile; t < num_tiles && ok; t += stride) {
       const Tile tl = tile_at<Kind, Mode>(args, off, first, t);
@@ -249,6 +250,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         __syncwarp();
+        if (kTails && k + 64 > tl.red) {
+          tails |= 1u << stage;
+          tail_odd ^= 1u << stage;
+        }
         ++fills;
         if (++stage == C::kStages) {
           stage = 0;
@@ -257,6 +262,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (!ok && leader) drain_copies(full, C::kStages, fills);  // the leader's barriers count both CTAs' copies
+    if (kTails && !ok && !leader) {                         // but for the peer's tails
+      for (int i = 0; i < C::kStages; ++i)
+        if (tails >> i & 1u) drain_copies(&tail_full[i], 1, 2 - (tail_odd >> i & 1u));
+    }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issuer
     int stage = 0, abuf = 0;
