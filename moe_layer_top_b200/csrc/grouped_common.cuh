@@ -343,35 +343,61 @@ __device__ __forceinline__ void store_columns16(const float (&v)[16], void* out,
 
 // The sum of a split tile: every CTA of the cluster has its partial sums [rows][kPartialPitch] at `smem`; CTA `cta`
 // adds its part of the elements up in rank order (so the result does not depend on timing) and stores them at
-// out[at + row * ldo + column], cols a multiple of 8.
+// out[at + row * ldo + column], cols a multiple of 8.  Eight reads of other CTAs' shared memory are under way at a
+// time: one after the other their latency is most of a small product's time (333 x 2056 x 1616 bf16 11.6 us that way).
+template <int kThreads, int kSplits>
+__device__ __forceinline__ void add_partials_of(const uint8_t* smem, int cta, int rows, int cols, void* out,
+                                                long long at, long long ldo, bool out_f32, bool accumulate) {
+  constexpr int kItems = 8 / kSplits;
+  const int quads = cols / 4, n = rows * quads;
+  uint32_t part[kSplits];
+#pragma unroll
+  for (int s = 0; s < kSplits; ++s) part[s] = in_cta(smem, s);
+  for (int i0 = cta * kThreads + threadIdx.x; i0 < n; i0 += kItems * kSplits * kThreads) {
+    float4 p[kItems][kSplits];
+#pragma unroll
+    for (int u = 0; u < kItems; ++u) {
+      const int i = i0 + u * kSplits * kThreads;
+      const int r = i / quads, c = (i - r * quads) * 4;
+#pragma unroll
+      for (int s = 0; s < kSplits; ++s)
+        if (i < n) p[u][s] = load_in_cluster(part[s] + (r * kPartialPitch + c) * 4);
+    }
+#pragma unroll
+    for (int u = 0; u < kItems; ++u) {
+      const int i = i0 + u * kSplits * kThreads;
+      if (i >= n) break;
+      const int r = i / quads, c = (i - r * quads) * 4;
+      float4 v = p[u][0];
+#pragma unroll
+      for (int s = 1; s < kSplits; ++s) {
+        v.x += p[u][s].x;
+        v.y += p[u][s].y;
+        v.z += p[u][s].z;
+        v.w += p[u][s].w;
+      }
+      const long long o = at + r * ldo + c;
+      if (out_f32) {
+        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(out) + o);
+        if (accumulate) {
+          const float4 b = *dst;
+          v = make_float4(b.x + v.x, b.y + v.y, b.z + v.z, b.w + v.w);
+        }
+        *dst = v;
+      } else {
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out) + o) =
+            make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+      }
+    }
+  }
+}
+
 template <int kThreads>
 __device__ __forceinline__ void add_partials(const uint8_t* smem, int cta, int splits, int rows, int cols, void* out,
                                              long long at, long long ldo, bool out_f32, bool accumulate) {
-  const int quads = cols / 4;
-  for (int i = cta * kThreads + threadIdx.x; i < rows * quads; i += splits * kThreads) {
-    const int r = i / quads, c = (i - r * quads) * 4;
-    const uint8_t* mine = smem + (r * kPartialPitch + c) * 4;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s = 0; s < splits; ++s) {
-      const float4 p = load_in_cluster(in_cta(mine, s));
-      v.x += p.x;
-      v.y += p.y;
-      v.z += p.z;
-      v.w += p.w;
-    }
-    const long long o = at + r * ldo + c;
-    if (out_f32) {
-      float4* dst = reinterpret_cast<float4*>(static_cast<float*>(out) + o);
-      if (accumulate) {
-        const float4 b = *dst;
-        v = make_float4(b.x + v.x, b.y + v.y, b.z + v.z, b.w + v.w);
-      }
-      *dst = v;
-    } else {
-      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out) + o) =
-          make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
-    }
-  }
+  if (splits == 2) add_partials_of<kThreads, 2>(smem, cta, rows, cols, out, at, ldo, out_f32, accumulate);
+  else if (splits == 4) add_partials_of<kThreads, 4>(smem, cta, rows, cols, out, at, ldo, out_f32, accumulate);
+  else add_partials_of<kThreads, 8>(smem, cta, rows, cols, out, at, ldo, out_f32, accumulate);
 }
 
 // Descriptor of an MN-major operand written by TMA with the 128-byte swizzle
