@@ -13,7 +13,7 @@
 // of the group the N side, which comes in steps of 16: a tile of a few rows
 // costs the tensor core little (a 128 x 128 tile of 2 rows held the memory
 // stream back: 512 rows over 256 groups of 7168 x 2048 took 613 us that way,
-// 500 this way).  An epilogue thread holds one column of up to 64 rows; the
+// 500 this way, and 467, 0.99 of HBM, with the deeper ring below).  An epilogue thread holds one column of up to 64 rows; the
 // rows' factors are read from shared memory, the same for all lanes.
 // kSplit: a cluster of up to eight CTAs shares the K blocks of one such tile,
 // each leaves its partial sums in shared memory and all add a part of them
@@ -41,14 +41,21 @@ constexpr int kThreads = 384;
 constexpr int kBatch = 4, kBatches = 3;
 constexpr int kScaleBytes = kBatches * kBatch * 128 * 4;
 constexpr int kTile = 128;            // columns, and most rows, of a tile
-constexpr int kStageBytes = 32768;    // 128 weight rows and up to 128 rows x 128 bytes
 constexpr int kAccBufs = 4;
 constexpr int kTmemCols = kAccBufs * kTile;
 constexpr int kHalf = kTile / 2;      // most rows of an epilogue warpgroup
-constexpr int kStages = (kSmemMax - 1024 - kGroupedReserve - kScaleBytes) / kStageBytes;
-constexpr size_t kSmemBytes = static_cast<size_t>(kStages) * kStageBytes + kScaleBytes + kGroupedReserve + 1024;
-static_assert(kStages >= 4, "ring depth");
-static_assert(kStages * kStageBytes >= 128 * kPartialPitch * 4, "partial sums fit the ring");
+// K blocks lie one behind the other in a ring of bytes, each as long as its tile's rows need (128 weight rows and a
+// box of 16 to 128 rows, 128 bytes each): eleven blocks of up to 16 rows are under way at a time, six of 128 (4096
+// skewed rows over 256 groups of 7168 x 2048: 571 us, 593 with six of any size; 512 rows 467 and 497 us).  kSplit,
+// whose CTAs all start on their only tile at once, has six of any size: more only delay the first (1 x 4096 x 7168:
+// 9.9 us instead of 9.4).
+constexpr int kWeightBytes = 16384;
+constexpr int kMostBytes = kWeightBytes + 128 * 128;  // of a block
+constexpr int kRingBytes = (kSmemMax - 1024 - kGroupedReserve - kScaleBytes) / 2048 * 2048;
+constexpr int kMostStages = 12;                       // blocks in the ring
+constexpr size_t kSmemBytes = static_cast<size_t>(kRingBytes) + kScaleBytes + kGroupedReserve + 1024;
+static_assert(kRingBytes >= 6 * kMostBytes, "ring depth");
+static_assert(kRingBytes >= 128 * kPartialPitch * 4, "partial sums fit the ring");
 
 struct Args {
   int M, G, N;
@@ -75,21 +82,28 @@ __device__ __forceinline__ Tile tile_at(const Args& a, const int* off, const int
   const int i = t - first[r.g];
   const int row0 = off[r.g], rows = off[r.g + 1] - row0;
   const int parts = (rows + kTile - 1) / kTile;
-  r.n = ((rows + parts - 1) / parts + 15) / 16 * 16;  // equal parts, <= kTile
+  const int each = ((rows + parts - 1) / parts + 15) / 16 * 16;  // equal parts, <= kTile
   const int p = i / a.n_tiles;
   r.col0 = (i - p * a.n_tiles) * kTile;
-  r.row0 = row0 + p * r.n;
-  r.rows = min(r.n, rows - p * r.n);  // at least one: rows > (parts - 1) * kTile >= (parts - 1) * n
+  r.row0 = row0 + p * each;
+  r.rows = min(each, rows - p * each);  // at least one: rows > (parts - 1) * kTile >= (parts - 1) * each
+  r.n = (r.rows + 15) / 16 * 16;        // (no more than the box that holds the rows)
   return r;
+}
+
+// bytes that are loaded for one K block of a tile
+__device__ __forceinline__ int block_bytes(const Tile& tl) {
+  return kWeightBytes + row_map_rows(row_map_index(tl.rows)) * 128;
 }
 
 template <bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_fp8_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ CUtensorMap tm_w,
                        const Args args) {
+  constexpr int kStages = kSplit ? 6 : kMostStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float* factors = reinterpret_cast<float*>(smem + static_cast<size_t>(kStages) * kStageBytes);
+  float* factors = reinterpret_cast<float*>(smem + kRingBytes);
   uint8_t* reserve = reinterpret_cast<uint8_t*>(factors) + kScaleBytes;
   uint64_t* full = reinterpret_cast<uint64_t*>(reserve);
   uint64_t* empty = full + kStages;
@@ -100,10 +114,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* drain = factor_empty + kBatches;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* lengths = reinterpret_cast<int*>(reserve + 512);  // of the ring's blocks (the producer's own)
   int* scan = reinterpret_cast<int*>(reserve + 640);
   int* off = reinterpret_cast<int*>(reserve + 1024);
   int* first = off + kMaxGroups + 4;
-  static_assert((2 * kStages + 2 * kAccBufs + 2 * kBatches + 1) * 8 + 8 <= 640, "barriers overlap the scan buffer");
+  static_assert((2 * kStages + 2 * kAccBufs + 2 * kBatches + 1) * 8 + 8 <= 512, "barriers overlap the lengths");
+  static_assert(kMostStages * 4 <= 128, "lengths overlap the scan buffer");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cta = kSplit ? static_cast<int>(cluster_rank()) : 0;
@@ -144,55 +160,84 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------------ producer
     const uint64_t pol = policy_evict_normal();
     int stage = 0;
-    uint32_t phase = 0;
     long long fills = 0;
+    int pos = 0, used = 0, held = 0;  // where the next block goes; bytes and blocks not yet given back
+    int oldest = 0;
+    uint32_t phase = 0;               // of the oldest block's barrier (kSplit: of the stage's)
     bool ok = true;
     for (int t = first_tile; t < num_tiles && ok; t += stride) {
       const Tile tl = tile_at(args, off, first, t);
-      const int box = row_map_index(tl.rows);  // rounded up to a multiple of 16 it still fits the box
-      const uint32_t bytes = row_map_rows(box) * 128 + 16384;
+      const int box = row_map_index(tl.rows);
+      const int bytes = block_bytes(tl);
       for (int kb = kb0; kb < kb1; ++kb) {
-        ok = warp_wait_bar(&empty[stage], phase ^ 1u, abort_flag, args.status, kWhereGroupedProducer);
-        if (!ok) break;
+        if constexpr (kSplit) {
+          ok = warp_wait_bar(&empty[stage], phase ^ 1u, abort_flag, args.status, kWhereGroupedProducer);
+          if (!ok) break;
+          pos = stage * kMostBytes;
+        } else {
+          const bool wrap = pos + bytes > kRingBytes;  // a block lies in one piece; the gap before it is its own
+          const int gap = wrap ? kRingBytes - pos : 0;
+          while (held == kStages || used + gap + bytes > kRingBytes) {
+            ok = warp_wait_bar(&empty[oldest], phase, abort_flag, args.status, kWhereGroupedProducer);
+            if (!ok) break;
+            used -= lengths[oldest];
+            --held;
+            if (++oldest == kStages) {
+              oldest = 0;
+              phase ^= 1u;
+            }
+          }
+          if (!ok) break;
+          if (wrap) pos = 0;
+          __syncwarp();  // the length just read may be that of the slot written next
+          if (elect_lane()) lengths[stage] = gap + bytes;
+          used += gap + bytes;
+          ++held;
+        }
         if (elect_lane()) {
-          uint8_t* a = smem + static_cast<size_t>(stage) * kStageBytes;
+          uint8_t* a = smem + pos;
           const uint32_t bar = smem_u32(&full[stage]);
           mbar_arrive_expect_tx(&full[stage], bytes);
           load_3d<false>(a, &tm_w, bar, kb * 128, tl.col0, tl.g, pol);
-          load_2d<false>(a + 16384, &tm_x.map[box], bar, kb * 128, tl.row0, pol);
+          load_2d<false>(a + kWeightBytes, &tm_x.map[box], bar, kb * 128, tl.row0, pol);
         }
         __syncwarp();
+        pos += bytes;
         ++fills;
         if (++stage == kStages) {
           stage = 0;
-          phase ^= 1u;
+          if (kSplit) phase ^= 1u;
         }
       }
     }
     if (!ok) drain_copies(full, kStages, fills);
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issuer
-    int stage = 0, abuf = 0;
+    int stage = 0, pos = 0, abuf = 0;
     uint32_t phase = 0, aphase = 0;
     bool ok = true;
     for (int t = first_tile; t < num_tiles && ok; t += stride) {
       const Tile tl = tile_at(args, off, first, t);
+      const int bytes = block_bytes(tl);
       const uint32_t idesc = make_idesc(kTile, 0, true) | (static_cast<uint32_t>(tl.n >> 3) << 17);
       for (int kb = kb0; kb < kb1; ++kb) {
         ok = warp_wait_bar(&acc_empty[abuf], aphase ^ 1u, abort_flag, args.status, kWhereGroupedMma) &&
              warp_wait_bar(&full[stage], phase, abort_flag, args.status, kWhereGroupedMma);
         if (!ok) break;
         tc_fence_after();
+        if (kSplit) pos = stage * kMostBytes;  // as the producer does
+        else if (pos + bytes > kRingBytes) pos = 0;
         if (elect_lane()) {
           const uint32_t d = tmem_base + static_cast<uint32_t>(abuf * kTile);
-          const uint32_t a = smem_u32(smem + static_cast<size_t>(stage) * kStageBytes);
-          const uint64_t ad = smem_desc_sw128(a), bd = smem_desc_sw128(a + 16384);
+          const uint32_t a = smem_u32(smem + pos);
+          const uint64_t ad = smem_desc_sw128(a), bd = smem_desc_sw128(a + kWeightBytes);
 #pragma unroll
           for (int s = 0; s < 4; ++s) mma_fp8(d, ad + 2 * s, bd + 2 * s, idesc, s > 0 ? 1u : 0u);  // + 32 bytes
           mma_commit(&acc_full[abuf]);
           mma_commit(&empty[stage]);
         }
         __syncwarp();
+        pos += bytes;
         if (++abuf == kAccBufs) {
           abuf = 0;
           aphase ^= 1u;
