@@ -586,7 +586,11 @@ cudaError_t dispatch(const GroupedProblem& p, cudaStream_t s) {
     return Kind == kGroupedDw ? p.G * m_tiles * ((p.K + tile - 1) / tile) : row_tiles(p.M, p.G, tile) * m_tiles;
   };
   const long long red = Kind == kGroupedFwd ? p.K : (Kind == kGroupedDx ? p.N : p.M / p.G);
-  const int splits = choose_splits(tiles(128), p.num_sms, static_cast<int>((red + 63) / 64));
+  using C = Cfg<Kind, kModeSplit>;
+  int splits;
+  const cudaError_t e = choose_splits<grouped_bf16_kernel<Kind, kModeSplit>>(
+      tiles(128), p.num_sms, static_cast<int>((red + 63) / 64), kThreads, C::kSmemBytes, &splits);
+  if (e != cudaSuccess) return e;
   if (splits > 1) return launch_tiles<Kind, kModeSplit>(p, splits, s);
   // a stage takes a pair about as long for its 256 x 256 tile as a CTA for its 128 x 128, so the pairs win where
   // the larger tiles do not need more rounds over the SMs
@@ -654,12 +658,6 @@ bool make_row_maps(RowMaps* maps, const void* base, long long rows, long long co
   for (int i = 0; i <= most; ++i)
     if (!make_grouped_map(&maps->map[i], base, 0, rows, cols, ld, elem_bytes, row_map_rows(i))) return false;
   return true;
-}
-
-int choose_splits(long long tiles, int sms, int stages) {
-  int splits = 1;
-  while (splits < 8 && tiles * splits * 2 <= sms && stages >= 4 * splits * 2) splits *= 2;
-  return splits;
 }
 
 cudaError_t launch_grouped(const GroupedProblem& p, cudaStream_t stream) {

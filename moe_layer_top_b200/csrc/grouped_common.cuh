@@ -345,32 +345,33 @@ __device__ __forceinline__ void store_columns16(const float (&v)[16], void* out,
 // adds its part of the elements up in rank order (so the result does not depend on timing) and stores them at
 // out[at + row * ldo + column], cols a multiple of 8.  Eight reads of other CTAs' shared memory are under way at a
 // time: one after the other their latency is most of a small product's time (333 x 2056 x 1616 bf16 11.6 us that way).
-template <int kThreads, int kSplits>
-__device__ __forceinline__ void add_partials_of(const uint8_t* smem, int cta, int rows, int cols, void* out,
+template <int kThreads, int kMost>
+__device__ __forceinline__ void add_partials_of(const uint8_t* smem, int cta, int splits, int rows, int cols, void* out,
                                                 long long at, long long ldo, bool out_f32, bool accumulate) {
-  constexpr int kItems = 8 / kSplits;
-  const int quads = cols / 4, n = rows * quads;
-  uint32_t part[kSplits];
+  constexpr int kItems = 8 / kMost;
+  const int quads = cols / 4, n = rows * quads, step = splits * kThreads;
+  uint32_t part[kMost];
 #pragma unroll
-  for (int s = 0; s < kSplits; ++s) part[s] = in_cta(smem, s);
-  for (int i0 = cta * kThreads + threadIdx.x; i0 < n; i0 += kItems * kSplits * kThreads) {
-    float4 p[kItems][kSplits];
+  for (int s = 0; s < kMost; ++s) part[s] = in_cta(smem, s < splits ? s : 0);
+  for (int i0 = cta * kThreads + threadIdx.x; i0 < n; i0 += kItems * step) {
+    float4 p[kItems][kMost];
 #pragma unroll
     for (int u = 0; u < kItems; ++u) {
-      const int i = i0 + u * kSplits * kThreads;
+      const int i = i0 + u * step;
       const int r = i / quads, c = (i - r * quads) * 4;
 #pragma unroll
-      for (int s = 0; s < kSplits; ++s)
-        if (i < n) p[u][s] = load_in_cluster(part[s] + (r * kPartialPitch + c) * 4);
+      for (int s = 0; s < kMost; ++s)
+        if (i < n && s < splits) p[u][s] = load_in_cluster(part[s] + (r * kPartialPitch + c) * 4);
     }
 #pragma unroll
     for (int u = 0; u < kItems; ++u) {
-      const int i = i0 + u * kSplits * kThreads;
+      const int i = i0 + u * step;
       if (i >= n) break;
       const int r = i / quads, c = (i - r * quads) * 4;
       float4 v = p[u][0];
 #pragma unroll
-      for (int s = 1; s < kSplits; ++s) {
+      for (int s = 1; s < kMost; ++s) {
+        if (s >= splits) break;
         v.x += p[u][s].x;
         v.y += p[u][s].y;
         v.z += p[u][s].z;
@@ -395,9 +396,9 @@ __device__ __forceinline__ void add_partials_of(const uint8_t* smem, int cta, in
 template <int kThreads>
 __device__ __forceinline__ void add_partials(const uint8_t* smem, int cta, int splits, int rows, int cols, void* out,
                                              long long at, long long ldo, bool out_f32, bool accumulate) {
-  if (splits == 2) add_partials_of<kThreads, 2>(smem, cta, rows, cols, out, at, ldo, out_f32, accumulate);
-  else if (splits == 4) add_partials_of<kThreads, 4>(smem, cta, rows, cols, out, at, ldo, out_f32, accumulate);
-  else add_partials_of<kThreads, 8>(smem, cta, rows, cols, out, at, ldo, out_f32, accumulate);
+  if (splits == 2) add_partials_of<kThreads, 2>(smem, cta, 2, rows, cols, out, at, ldo, out_f32, accumulate);
+  else if (splits <= 4) add_partials_of<kThreads, 4>(smem, cta, splits, rows, cols, out, at, ldo, out_f32, accumulate);
+  else add_partials_of<kThreads, 8>(smem, cta, splits, rows, cols, out, at, ldo, out_f32, accumulate);
 }
 
 // Descriptor of an MN-major operand written by TMA with the 128-byte swizzle
@@ -544,11 +545,46 @@ cudaError_t prepare_kernel(size_t smem, int regs) {
   return e;
 }
 
+// Clusters of `size` CTAs of the prepared kernel that are resident at once (the SMs of a GPC need not divide evenly);
+// asked once per size and device.
+template <auto kKernel>
+cudaError_t resident_clusters(int threads, int size, size_t smem, int* count) {
+  static int fit[64][9] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || size > 8) return cudaErrorInvalidValue;
+  if (fit[dev][size] == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.gridDim = dim3(static_cast<unsigned>(size));
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = static_cast<unsigned>(size);
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if ((e = cudaOccupancyMaxActiveClusters(&n, kKernel, &cfg)) != cudaSuccess) return e;
+    fit[dev][size] = n > 0 ? n : 1;
+  }
+  *count = fit[dev][size];
+  return cudaSuccess;
+}
+
 // Launch clusters of `size` CTAs with programmatic stream serialisation (see launch_pdl).  persistent: no more than
-// are resident at once (the SMs of a GPC need not divide evenly), always of the same size.
+// are resident at once.
 template <auto kKernel, typename... Args>
 cudaError_t launch_clusters(int threads, int size, long long clusters, bool persistent, size_t smem,
                             cudaStream_t stream, const Args&... args) {
+  if (persistent) {
+    int most = 0;
+    const cudaError_t e = resident_clusters<kKernel>(threads, size, smem, &most);
+    if (e != cudaSuccess) return e;
+    if (clusters > most) clusters = most;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = smem;
@@ -561,22 +597,6 @@ cudaError_t launch_clusters(int threads, int size, long long clusters, bool pers
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  if (persistent) {
-    static int fit[64] = {};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev >= 64) return cudaErrorInvalidDevice;
-    if (fit[dev] == 0) {
-      cfg.numAttrs = 1;
-      cfg.gridDim = dim3(static_cast<unsigned>(size));
-      int n = 0;
-      e = cudaOccupancyMaxActiveClusters(&n, kKernel, &cfg);
-      if (e != cudaSuccess) return e;
-      fit[dev] = n > 0 ? n : 1;
-    }
-    if (clusters > fit[dev]) clusters = fit[dev];
-  }
   cfg.numAttrs = 2;
   cfg.gridDim = dim3(static_cast<unsigned>(clusters * size));
   return cudaLaunchKernelEx(&cfg, kKernel, args...);
@@ -591,8 +611,23 @@ inline long long row_tiles(long long M, long long G, int tile) {
   return n > groups ? n : groups;
 }
 
-// CTAs that share a tile's reduction: as many (1, 2, 4, 8) as leave each at least four stages and do not make more
-// CTAs than SMs.
-int choose_splits(long long tiles, int sms, int stages);
+// CTAs that share a tile's reduction: as many as leave each at least four stages and let all clusters be resident at
+// once; 1 if there is nothing to share.  kKernel is prepared if more than 1.  (Sixteen clusters of eight need not fit
+// 148 SMs: one row by 2048 x 7168 in FP8 takes 12.5 us in two rounds of clusters of eight and 7.7 us in one of seven.)
+template <auto kKernel>
+cudaError_t choose_splits(long long tiles, int sms, int stages, int threads, size_t smem, int* splits) {
+  *splits = 1;
+  for (int s = 8; s > 1; --s) {
+    if (tiles * s > sms || stages < 4 * s) continue;
+    int most = 0;
+    cudaError_t e = prepare_kernel<kKernel>(smem, 0);
+    if (e == cudaSuccess) e = resident_clusters<kKernel>(threads, s, smem, &most);
+    if (e != cudaSuccess) return e;
+    if (tiles > most) continue;
+    *splits = s;
+    break;
+  }
+  return cudaSuccess;
+}
 
 }  // namespace moe

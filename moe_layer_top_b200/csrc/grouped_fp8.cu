@@ -422,7 +422,10 @@ cudaError_t launch_columns(const GroupedProblem& p, int splits, cudaStream_t s) 
 
 cudaError_t launch_grouped_fp8(const GroupedProblem& p, cudaStream_t stream) {
   const long long single = row_tiles(p.M, p.G, 128) * ((p.N + 127) / 128);
-  const int splits = choose_splits(single, p.num_sms, (p.K + 127) / 128);
+  int splits;
+  const cudaError_t e = choose_splits<grouped_fp8_kernel<true>>(single, p.num_sms, (p.K + 127) / 128, kThreads,
+                                                                kSmemBytes, &splits);
+  if (e != cudaSuccess) return e;
   if (splits > 1) return launch_columns<true>(p, splits, stream);
   // A pair computes its 256 x 256 tile in the time that a CTA takes for 128 x 128, so it wins unless the larger tiles
   // leave SMs idle (N = 4096, K = 7168: 512 rows 32 us in pairs and 34 in single tiles, 1024 rows 33 and 64 us) or

@@ -107,6 +107,34 @@ def test_dx(sizes, N, K, dtype):
                 off, M, N)
 
 
+@pytest.mark.parametrize("tiles", [10, 18, 20, 24, 29, 37, 49, 74])
+@pytest.mark.parametrize("M", [5, 77])
+def test_every_number_of_parts_of_a_reduction(tiles, M):
+    """Few tiles with long reductions, shared by 8, 7, 6, 5, 4, 3 and 2 CTAs (or fewer, where a GPU holds fewer
+    clusters of that size at once)."""
+    n, k = 128 * tiles - 40, 2072
+    off = offsets_of([M])
+    x, w = _rows(11, M, k), _randn(12, 1, n, k, std=0.1)
+    y = _forward(x, w, off, n, M)
+    _check_rows(y, lambda g, a, b: (x[a:b].double() @ w[g].double().t(),
+                                    x[a:b].double().abs() @ w[g].double().abs().t()), off, M, k)
+    dy, wt = _rows(13, M, k), _randn(14, 1, k, n, std=0.1)
+    dx = torch.full((M, n), 7.0, dtype=torch.bfloat16, device="cuda")
+    ops.grouped_matmul_dx(dy, wt, off, out=dx)
+    _check_rows(dx, lambda g, a, b: (dy[a:b].double() @ wt[g].double(), dy[a:b].double().abs() @ wt[g].double().abs()),
+                off, M, k)
+    a, b = _rows(15, 27 * M + 2000, n), _rows(16, 27 * M + 2000, 120)
+    dw = ops.grouped_matmul_dw(a, b, None, out_dtype=torch.float32)
+    ref, mag = a.double().t() @ b.double(), a.double().abs().t() @ b.double().abs()
+    assert_within(dw[0], ref, product_bound(ref, mag, a.shape[0], torch.float32))
+    k = 4112
+    (q, qs), (c, cs) = quantize_rows(_rows(17, M, k)), quantize_weight(_randn(18, n, k, std=0.1))
+    y = ops.matmul_fp8(q, qs, c, cs)
+    xv, wv = row_values(q, qs), weight_values(c, cs)
+    ref, mag = xv @ wv.t(), xv.abs() @ wv.abs().t()
+    assert_within(y, ref, product_bound(ref, mag, k, torch.bfloat16, True))
+
+
 @pytest.mark.parametrize("sizes,N,K", _cases())
 @pytest.mark.parametrize("dtype,accumulate", [(torch.bfloat16, False), (torch.float32, False), (torch.float32, True)],
                          ids=["bf16", "fp32", "accumulate"])
