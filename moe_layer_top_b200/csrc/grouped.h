@@ -34,6 +34,8 @@ struct GroupedProblem {
 
 cudaError_t launch_grouped(const GroupedProblem& p, cudaStream_t stream);
 cudaError_t launch_grouped_fp8(const GroupedProblem& p, cudaStream_t stream);
-cudaError_t launch_grouped_fp8_pair(const GroupedProblem& p, cudaStream_t stream);
+// split: two pairs share a tile's K blocks; as many such clusters as fp8_pair_split_clusters says are resident at once
+cudaError_t launch_grouped_fp8_pair(const GroupedProblem& p, bool split, cudaStream_t stream);
+cudaError_t fp8_pair_split_clusters(int* count);
 
 }  // namespace moe

@@ -219,14 +219,15 @@ __device__ __forceinline__ void mma_fp8_for(uint32_t d, uint64_t a, uint64_t b, 
     mma_fp8(d, a, b, idesc, acc);
 }
 
-// arrive on `bar` of every CTA of the pair (or of this CTA) once this thread's MMAs so far are done
+// arrive on `bar` of every CTA of the pair (or of this CTA) once this thread's MMAs so far are done; `lead` is the
+// pair's first rank in its cluster
 template <bool kPair>
-__device__ __forceinline__ void commit_for(uint64_t* bar) {
+__device__ __forceinline__ void commit_for(uint64_t* bar, int lead = 0) {
   if constexpr (kPair)
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
             smem_u32(bar)),
-        "h"(static_cast<uint16_t>(3))
+        "h"(static_cast<uint16_t>(3 << lead))
         : "memory");
   else
     mma_commit(bar);
@@ -301,6 +302,11 @@ __device__ __forceinline__ float4 load_in_cluster(uint32_t addr) {
                : "r"(addr)
                : "memory");
   return v;
+}
+
+__device__ __forceinline__ void store_in_cluster(uint32_t addr, const float4& v) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+               : "memory");
 }
 
 // Stores 16 accumulator columns of tiles whose columns are output rows: lane `lane` holds column `col` of rows

@@ -433,7 +433,16 @@ cudaError_t launch_grouped_fp8(const GroupedProblem& p, cudaStream_t stream) {
   const int sms = p.num_sms, pairs = p.num_sms / 2;
   const long long pair = row_tiles(p.M, p.G, 256) * ((p.N + 255) / 256);
   const bool use_pair = p.M / p.G > 128 && (pair + pairs - 1) / pairs <= (single + sms - 1) / sms;
-  return use_pair ? launch_grouped_fp8_pair(p, stream) : launch_columns<false>(p, 1, stream);
+  // Few such tiles and a long reduction: two pairs share each one's K blocks (256 x 5120 x 7168: 24 us, 30 without;
+  // 640 x 2560 x 4096 17.7 and 19.7; 256 x 7168 x 2048 16 and 13).
+  bool split_pair = false;
+  if (p.M / p.G > 128 && 2 * pair <= pairs && p.K >= 32 * 128) {
+    int most = 0;
+    const cudaError_t err = fp8_pair_split_clusters(&most);
+    if (err != cudaSuccess) return err;
+    split_pair = pair <= most;
+  }
+  return use_pair || split_pair ? launch_grouped_fp8_pair(p, split_pair, stream) : launch_columns<false>(p, 1, stream);
 }
 
 }  // namespace moe

@@ -9,15 +9,19 @@
 // accumulators bounds the kernel: a K block takes about 830 cycles, of which
 // the products take 512, the rest is the way from commit over both CTAs'
 // epilogues back to the issuer, with room for two accumulators only
-// (8192 x 4096 x 7168: 218 us, 2200 TFLOP/s; a plain FP8 product without scales
+// (8192 x 4096 x 7168: 211 to 217 us, 2200 TFLOP/s; a plain FP8 product without scales
 // per block needs none of it and takes 168 us).
 //
 // Row tiles start at any row; a tile that runs past its group's end computes
 // rows of the next group and does not store them; no more rows than the group
 // has are loaded, rounded up to a box of 16, 32, 64, 96 or 128.
 //
+// kSplit: a cluster of four, two such pairs, each with half of the K blocks; one tile per cluster.  Each pair then
+// finishes one half of the columns: the sums of the other half go through distributed shared memory (pushed: reading
+// them from the other pair's took 28 us instead of 25 for 256 x 5120 x 7168).
+//
 // Persistent, three warpgroups per CTA: the first holds the TMA producer, the
-// MMA issuer (of the leader CTA) and two warps that multiply the scales and lay
+// MMA issuer (of a pair's leader) and two warps that multiply the scales and lay
 // the factors of four K blocks at a time into shared memory; the other two are
 // the epilogue and take over the registers that the first does without.  (An
 // epilogue thread must have no global load under way: its hand-offs wait for
@@ -29,7 +33,7 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 384;
-constexpr int kProducerRegs = 88, kEpilogueRegs = 208;  // 128 * 88 + 256 * 208 = 384 * 168, what the launch has
+constexpr int kProducerRegs = 104, kEpilogueRegs = 200;  // 128 * 104 + 256 * 200 = 384 * 168, what the launch has
 constexpr int kLaunchRegs = 168;
 // The scales' factors go through a ring of batches in shared memory: [column half][slot][K block][row].
 constexpr int kBatch = 4, kBatches = 3;
@@ -77,6 +81,7 @@ __device__ __forceinline__ Tile tile_at(const Args& a, const int* off, const int
   return r;
 }
 
+template <bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_fp8_pair_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ CUtensorMap tm_w,
                        const __grid_constant__ CUtensorMap tm_out, const Args args) {
@@ -100,7 +105,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   static_assert((2 * kStages + 2 * kAccBufs + 4 * kBatches + 1) * 8 + 8 <= 640, "barriers overlap the scan buffer");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = static_cast<int>(cluster_rank());  // half of the tile
+  const int cta = static_cast<int>(cluster_rank());
+  const int rank = cta & 1;                      // half of the tile
+  const int part = kSplit ? cta >> 1 : 0;        // half of the K blocks
+  const int lead = kSplit ? cta & ~1 : 0;        // the pair's leader in the cluster
   const bool leader = rank == 0;
   pdl_launch_dependents();
   if (threadIdx.x == 0) {
@@ -130,8 +138,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_barrier();  // the peer's barriers are initialised before any remote arrival
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const int first_tile = static_cast<int>(blockIdx.x) / 2, stride = static_cast<int>(gridDim.x) / 2;
-  const int kb_n = args.k_blocks;
+  constexpr int kCluster = kSplit ? 4 : 2;
+  const int first_tile = static_cast<int>(blockIdx.x) / kCluster;
+  const int stride = static_cast<int>(gridDim.x) / kCluster;  // kSplit: no cluster takes a second tile
+  const int kb0 = kSplit ? args.k_blocks * part / 2 : 0;
+  const int kb1 = kSplit ? args.k_blocks * (part + 1) / 2 : args.k_blocks;
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
@@ -151,13 +162,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int rows = loaded(rank);
         const CUtensorMap* map = &tm_x.map[rows > 0 ? row_map_index(rows) : 0];
         const uint32_t bytes = (loaded(0) + loaded(1)) * 128 + 32768;
-        for (int kb = 0; kb < kb_n; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           ok = warp_wait_bar(&empty[stage], phase ^ 1u, abort_flag, args.status, kWhereGroupedProducer);
           if (!ok) break;
           if (elect_lane()) {
             uint8_t* a = smem + static_cast<size_t>(stage) * kStageBytes;
             if (leader) mbar_arrive_expect_tx(&full[stage], bytes);
-            const uint32_t bar = in_cta(&full[stage], 0);
+            const uint32_t bar = in_cta(&full[stage], lead);
             if (rows > 0) load_2d<true>(a, map, bar, kb * 128, tl.row0 + 128 * rank, pol);
             load_3d<true>(a + 16384, &tm_w, bar, kb * 128, tl.col0 + 128 * rank, tl.g, pol);
           }
@@ -177,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t phase = 0, aphase = 0;
         bool ok = true;
         for (int t = first_tile; t < num_tiles && ok; t += stride) {
-          for (int kb = 0; kb < kb_n; ++kb) {
+          for (int kb = kb0; kb < kb1; ++kb) {
             // (the operands are there long before the accumulator is: wait for that last)
             const uint32_t d = tmem_base + static_cast<uint32_t>(abuf * kTile);
             const uint32_t a = smem_u32(smem + static_cast<size_t>(stage) * kStageBytes);
@@ -189,8 +200,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (elect_lane()) {
 #pragma unroll
               for (int s = 0; s < 4; ++s) mma_fp8_for<true>(d, ad + 2 * s, bd + 2 * s, kIdesc, s > 0 ? 1u : 0u);
-              commit_for<true>(&acc_full[abuf]);
-              commit_for<true>(&empty[stage]);
+              commit_for<true>(&acc_full[abuf], lead);
+              commit_for<true>(&empty[stage], lead);
             }
             __syncwarp();
             if (++abuf == kAccBufs) {
@@ -205,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // every MMA that the elected lanes issued has completed once `drain` flips
         // (waited on even after an abort: TMEM must not be freed under a running MMA)
-        if (elect_lane()) commit_for<true>(drain);
+        if (elect_lane()) commit_for<true>(drain, lead);
         __syncwarp();
         drain_mma(drain, args.status);
       }
@@ -223,11 +234,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float* x[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[i] = args.x_scale + tl.row0 + min(128 * rank + lane + 32 * i, tl.rows - 1);
-        for (int kb = 0; kb < kb_n; kb += kBatch) {
+        for (int kb = kb0; kb < kb1; kb += kBatch) {
           float xs[kBatch][4], ws[kBatch];
 #pragma unroll
           for (int j = 0; j < kBatch; ++j) {
-            const int k = min(kb + j, kb_n - 1);
+            const int k = min(kb + j, kb1 - 1);
             ws[j] = w[k];
 #pragma unroll
             for (int i = 0; i < 4; ++i) xs[j][i] = x[i][static_cast<long long>(k) * args.M];
@@ -249,6 +260,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+    __syncwarp();
+    if (kSplit) {  // where the pairs meet
+      cluster_barrier();
+      cluster_barrier();
+    }
   } else {
     // ------------------------------------------------------------------ epilogue
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpilogueRegs));
@@ -257,13 +273,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = 32 * q + lane;        // accumulator row
     uint8_t* out_box = staging + static_cast<size_t>(warp - 4) * 4096;
     const uint32_t lane_addr = (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(kCols * g);
-    const uint32_t empty_bar = in_cta(acc_empty, 0);
+    const uint32_t empty_bar = in_cta(acc_empty, lead);
     const float* my_factors = factors + g * kBatches * kBatch * 128 + row;
     uint32_t fphase = 0;
     int slot = 0;
     int abuf = 0;
     uint32_t aphase = 0;
-    bool ok = true;
+    bool ok = true, met = false;  // kSplit: met the other pair
     for (int t = first_tile; t < num_tiles && ok; t += stride) {
       const Tile tl = tile_at(args, off, first, t);
       const int rows = tl.rows - 128 * rank;            // of this CTA's half
@@ -272,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float acc[kCols];
 #pragma unroll
       for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
-      for (int kb = 0; kb < kb_n && ok; kb += kBatch) {
+      for (int kb = kb0; kb < kb1 && ok; kb += kBatch) {
         // the factors of the next blocks
         ok = warp_wait_bar(&factor_full[g * kBatches + slot], fphase, abort_flag, args.status, kWhereGroupedEpilogue);
         if (!ok) break;
@@ -287,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
-          if (kb + j >= kb_n) break;
+          if (kb + j >= kb1) break;
           ok = warp_wait_bar(&acc_full[abuf], aphase, abort_flag, args.status, kWhereGroupedEpilogue);
           if (!ok) break;
           tc_fence_after();
@@ -321,6 +337,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) break;
+      if constexpr (kSplit) {
+        // each pair finishes one column half: the other half's sums go to the CTA with the same rows in the other
+        // pair, into its ring, which is idle behind the first barrier
+        const int mine = row * kPartialPitch * 4;
+        __syncwarp();
+        cluster_barrier();
+        if (live && g != part) {
+          const uint32_t p = in_cta(smem + mine, cta ^ 2);
+#pragma unroll
+          for (int c = 0; c < kCols; c += 4)
+            store_in_cluster(p + 4 * c, make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]));
+        }
+        __syncwarp();
+        cluster_barrier();
+        met = true;
+        if (g != part) continue;
+        if (live) {
+          const float4* p = reinterpret_cast<const float4*>(smem + mine);
+#pragma unroll
+          for (int c = 0; c < kCols; c += 4) {
+            const float4 v = p[c / 4];
+            acc[c] += v.x;
+            acc[c + 1] += v.y;
+            acc[c + 2] += v.z;
+            acc[c + 3] += v.w;
+          }
+        }
+      }
       if (!live) continue;
       if (32 * q + 32 <= rows) {
         // 128 bytes of each row go through shared memory as one TMA store of the warp's 32 rows (it leaves out
@@ -377,6 +421,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (lane == 0) bulk_wait_all();
+    __syncwarp();
+    if (kSplit && !met) {
+      cluster_barrier();
+      cluster_barrier();
+    }
   }
 
   __syncwarp();
@@ -388,10 +437,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-}  // namespace
-
-cudaError_t launch_grouped_fp8_pair(const GroupedProblem& p, cudaStream_t s) {
-  constexpr auto kern = grouped_fp8_pair_kernel;
+template <bool kSplit>
+cudaError_t launch_tiles(const GroupedProblem& p, cudaStream_t s) {
+  constexpr auto kern = grouped_fp8_pair_kernel<kSplit>;
   // the register split waits for ever if the kernel is launched with fewer registers than it redistributes
   const cudaError_t e = prepare_kernel<kern>(kSmemBytes, kLaunchRegs);
   if (e != cudaSuccess) return e;
@@ -415,7 +463,19 @@ cudaError_t launch_grouped_fp8_pair(const GroupedProblem& p, cudaStream_t s) {
       !make_store_map(&tm_out, p.out, 1, p.M, p.N, p.ldo, p.out_f32, 128))
     return cudaErrorInvalidValue;
   const long long tiles = (static_cast<long long>(p.M) / kTile + (p.M < p.G ? p.M : p.G)) * a.n_tiles;
-  return launch_clusters<kern>(kThreads, 2, tiles, true, kSmemBytes, s, tm_x, tm_w, tm_out, a);
+  return launch_clusters<kern>(kThreads, kSplit ? 4 : 2, tiles, !kSplit, kSmemBytes, s, tm_x, tm_w, tm_out, a);
+}
+
+}  // namespace
+
+cudaError_t launch_grouped_fp8_pair(const GroupedProblem& p, bool split, cudaStream_t s) {
+  return split ? launch_tiles<true>(p, s) : launch_tiles<false>(p, s);
+}
+
+cudaError_t fp8_pair_split_clusters(int* count) {
+  constexpr auto kern = grouped_fp8_pair_kernel<true>;
+  const cudaError_t e = prepare_kernel<kern>(kSmemBytes, kLaunchRegs);
+  return e != cudaSuccess ? e : resident_clusters<kern>(kThreads, 4, kSmemBytes, count);
 }
 
 }  // namespace moe

@@ -135,6 +135,20 @@ def test_every_number_of_parts_of_a_reduction(tiles, M):
     assert_within(y, ref, product_bound(ref, mag, k, torch.bfloat16, True))
 
 
+@pytest.mark.parametrize("sizes,N,K", [([200], 4872, 4112), ([450], 4104, 4480), ([150, 0, 301], 2056, 4240),
+                                       ([1, 500, 40], 2120, 4096)])
+def test_fp8_tiles_whose_reduction_two_pairs_share(sizes, N, K):
+    off = offsets_of(sizes, start=1)
+    M, G = int(off[-1]) + 2, len(sizes)
+    x, xs = quantize_rows(_rows(21, M, K))
+    w, ws = quantize_weight(_randn(22, G, N, K, std=0.1))
+    xv, wv = row_values(x, xs), weight_values(w, ws)
+    for dtype in (torch.bfloat16, torch.float32):
+        y = _forward(x, w, off, N, M, dtype=dtype, x_scale=xs, w_scale=ws)
+        _check_rows(y, lambda g, a, b: (xv[a:b] @ wv[g].t(), xv[a:b].abs() @ wv[g].abs().t()), off, M, K, fp8=True)
+        assert torch.equal(y, _forward(x, w, off, N, M, dtype=dtype, x_scale=xs, w_scale=ws))
+
+
 @pytest.mark.parametrize("sizes,N,K", _cases())
 @pytest.mark.parametrize("dtype,accumulate", [(torch.bfloat16, False), (torch.float32, False), (torch.float32, True)],
                          ids=["bf16", "fp32", "accumulate"])
