@@ -155,6 +155,23 @@ def test_backward(T, H, dres):
     assert torch.equal(again[0], dx) and torch.equal(again[1], dw)
 
 
+@pytest.mark.parametrize("T,H", [(1776, 5120), (1775, 5120), (1800, 5128), (14300, 520), (3552, 4096), (149, 8200),
+                                 (300, 12288), (1, 10240), (447, 16384)])
+def test_backward_with_rows_under_way(T, H):
+    """Where rows are copied ahead: one and two vectors per thread, blocks with equal and unequal numbers of rows,
+    every number of rows ahead, outputs in place."""
+    dy, s, w = _rows(14, T, H, 0.01, stride=H + 8), _rows(15, T, H, 2.0, stride=H + 16), _weight(H)
+    r = ops.rms_norm(s, w, EPS, rstd=True)["rstd"]
+    for d in (None, _rows(16, T, H, 0.01)):
+        dx, dw = ops.rms_norm_backward(dy, s, w, r, dresidual=d)
+        rx, mag, rw, wmag = _backward_reference(dy, s, w, r, d)
+        assert_within(dx, rx, rx.abs() * HALF_STEP[torch.bfloat16] + mag * FP32)
+        assert_within(dw, rw, wmag * (T + 2) * 2.0 ** -23)
+        place = dy.clone() if d is None else d
+        again = ops.rms_norm_backward(dy if d is not None else place, s, w, r, dresidual=d, dx=place)
+        assert torch.equal(again[0], dx) and torch.equal(again[1], dw)
+
+
 def test_backward_against_differences():
     """The gradient of sum(c * y) in double, by central differences of the definition."""
     T, H, h = 3, 24, 1e-5
