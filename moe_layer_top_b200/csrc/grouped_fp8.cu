@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int t = first_tile; t < num_tiles && ok; t += stride) {
       const Tile tl = tile_at(args, off, first, t);
-      const int half = tl.n / 2;          // this group's rows: [half * g, half * g + half), in chunks of 16
+      const int half = (tl.n / 2 + 15) / 16 * 16;  // this group's rows: [half * g, half * g + half), in chunks of 16
       const int col = tl.col0 + 32 * q + lane;
       const int mine = tl.col0 + 32 * q < args.N ? min(half, tl.rows - half * g) : 0;  // rows to store
       const int chunks = (max(mine, 0) + 15) / 16;
@@ -314,7 +314,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = warp_wait_bar(&acc_full[abuf], aphase, abort_flag, args.status, kWhereGroupedEpilogue);
           if (!ok) break;
           tc_fence_after();
-          // (a half of 8 or 24 rows reads 8 columns more: they lie in the buffer, their sums are not stored)
           const uint32_t d = tmem_base + lane_addr + static_cast<uint32_t>(abuf * kTile + half * g);
           uint32_t v[2][16];
           if (chunks > 0) tmem_ld16u(d, v[0]);
