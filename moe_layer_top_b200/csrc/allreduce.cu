@@ -216,10 +216,12 @@ __global__ void __launch_bounds__(kThreadsAr) combine_allreduce_kernel(const ArP
   }
 
   // 3. return once every chunk has been reduced: this rank's out is complete and no owner still
-  //    reads its partial
+  //    reads its partial (an owner may itself wait up to the limit in phase 2: a little longer
+  //    here, so that the status names that wait and not this one behind it)
   if (threadIdx.x == 0) {
+    const unsigned long long limit = P.timeout_ns + P.timeout_ns / 8;
     for (int c = cta; c < P.nchunks; c += P.ctas_per_rank)
-      if (!wait_epoch(R.flags + P.nchunks + c, P.epoch, abort_word, R.status, P.timeout_ns, kWhereArDone)) break;
+      if (!wait_epoch(R.flags + P.nchunks + c, P.epoch, abort_word, R.status, limit, kWhereArDone)) break;
   }
 }
 
