@@ -381,6 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (live) {
           const int chunks = (tl.valid + 15) / 16;
           for (int c = g; c < chunks; c += 2) {
+            __syncwarp();  // the stores branch by lane; a TMEM load wants the warp converged
             float v[16];
             if (any) {
               uint32_t u[16];
@@ -436,6 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         for (int c = 0; !kSplit && c < end; c += step) {
+          __syncwarp();  // as above: one lane stores
           const int col = g * kCols + c;
           uint4 piece[4];
           if (args.out_f32) {

@@ -96,7 +96,10 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   return r;
 }
 
+// All threads of the cluster take part.  The aligned form wants whole warps that are converged, which loops and
+// branches with a count of their own per lane in front of it do not promise.
 __device__ __forceinline__ void cluster_barrier() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
@@ -187,6 +190,7 @@ __device__ __forceinline__ void tmem_alloc_for(uint32_t* dst_smem, uint32_t ncol
 
 template <bool kPair>
 __device__ __forceinline__ void tmem_free_for(uint32_t taddr, uint32_t ncols) {
+  __syncwarp();  // an aligned instruction, as the barriers above
   if constexpr (kPair)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
   else
