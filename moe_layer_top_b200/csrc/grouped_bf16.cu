@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             steps = (tl.red - k + 15) / 16;
             clear_tail(st, tl.red - k);
             if constexpr (kTails) {
-              ok = warp_wait_bar(&peer_full[stage], tails >> stage & 1u, abort_flag, args.status, kWhereGroupedMma);
+              ok = warp_wait_peer(&peer_full[stage], tails >> stage & 1u, abort_flag, args.status, kWhereGroupedMma);
               if (!ok) break;
               tails ^= 1u << stage;
             }

@@ -50,6 +50,22 @@ __device__ __forceinline__ bool warp_wait_bar(uint64_t* bar, uint32_t parity, vo
   return __all_sync(0xffffffffu, ok);
 }
 
+// The same for a barrier that a thread of another CTA arrives on behind writes of its own (arrive_in_cluster_release):
+// acquired at cluster scope, or the writes would not be ordered.
+__device__ __forceinline__ bool warp_wait_peer(uint64_t* bar, uint32_t parity, volatile int* abort, int* status,
+                                               int where) {
+  if (!warp_wait_bar(bar, parity, abort, status, where)) return false;
+  uint32_t ok;  // true at once: the phase is over, and the next one begins when this thread goes on
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return true;
+}
+
 // One lane of a converged warp.  The producer and the issuer walk as whole warps and elect a lane for each batch of
 // instructions: what a warp computes alike then stays in uniform registers, where a loop inside `if (lane == 0)`
 // moves every descriptor and address there for each instruction (about 100 cycles per TMA or MMA instruction).

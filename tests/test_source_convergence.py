@@ -45,3 +45,12 @@ def test_tmem_loads_behind_stores_that_branch_by_lane():
     assert len(loops) == 2
     for body in loops:
         assert 0 <= body.find("__syncwarp()") < body.index("tmem_ld")
+
+
+def test_a_hand_over_between_two_ctas_is_acquired_at_cluster_scope():
+    """The peer arrives on peer_full behind writes to its own shared memory (release at cluster scope): a wait that
+    acquires for its own CTA only does not order them."""
+    common, kernel = _source("grouped_common.cuh"), _source("grouped_bf16.cu")
+    assert "arrive_in_cluster_release(in_cta(&peer_full[stage], 0))" in kernel
+    waits = re.findall(r"(\w+)\(&peer_full\[stage\]", kernel)
+    assert waits and all("acquire.cluster" in _block(common, common.index(f"bool {w}(")) for w in set(waits) - {"in_cta"})
