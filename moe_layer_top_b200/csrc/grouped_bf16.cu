@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Tile tl = tile_at<Kind, Mode>(args, off, first, t);
         next_stage(tl.red / 64);
         if (tl.red % 64 == 0) continue;
-        ok = warp_wait_bar(&tail_full[stage], tails >> stage & 1u, abort_flag, args.status, kWhereGroupedMma);
+        ok = warp_wait_bar(&tail_full[stage], tails >> stage & 1u, abort_flag, args.status, kWhereGroupedMma, &empty[0]);
         if (!ok) break;
         tails ^= 1u << stage;
         clear_tail(smem + static_cast<size_t>(stage) * C::kStageBytes, tl.red % 64);
@@ -373,7 +373,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t d = tmem_base + lane_addr + static_cast<uint32_t>(abuf * C::kNTile);
       const bool any = red_begin(tl) < red_end(tl);  // otherwise there is no accumulator: zeros
       if (any) {
-        if (!warp_wait_bar(&acc_full[abuf], aphase, abort_flag, args.status, kWhereGroupedEpilogue)) break;
+        // (over a tile's whole reduction: up to 2^30 long, seconds)
+        if (!warp_wait_bar(&acc_full[abuf], aphase, abort_flag, args.status, kWhereGroupedEpilogue, &empty[0])) break;
         tc_fence_after();
       }
       if constexpr (Kind != kGroupedDw) {
