@@ -518,7 +518,8 @@ MOE_API int moe_dequantize_rows_fp8(const uint8_t* codes, const float* scales, i
  *   NULL offsets with G = 1: one group of all rows.
  *   out_dtype: MOE_DTYPE_BF16 or MOE_DTYPE_FP32 (accumulate needs FP32).
  *   status: int32 device word that receives MOE_STATUS_WAIT_TIMEOUT | site if a
- *   bounded in-kernel wait runs out (never cleared here), or NULL.
+ *   bounded in-kernel wait runs out (never cleared here; the outputs are then
+ *   undefined), or NULL: the device's own word, see moe_operator_status().
  * 1 <= G <= 1024; M, N and K up to 2^30, N and K multiples of 8 (FP8: K of 16).
  * Accumulation is fp32 and each result is rounded once; results do not depend on timing.
  * The outputs must not overlap the inputs.
@@ -547,6 +548,17 @@ MOE_API int moe_grouped_matmul_dw(const void* dy, int64_t lddy, const void* x, i
 MOE_API int moe_matmul_fp8(const uint8_t* x, const float* x_scale, const uint8_t* w, const float* w_scale, int32_t M,
                            int32_t N, int32_t K, void* y, int64_t ldy, int32_t out_dtype, int32_t* status,
                            void* stream);
+
+/*
+ * The status word, one per device, of the stand-alone operators that are given
+ * none.  moe_operator_status() reads the current device's word (and with
+ * clear != 0 resets it): MOE_STATUS_OK, or what the first failure since the
+ * last reset left.  SYNCHRONISES `stream`, and sees the calls enqueued on it
+ * before.  moe_operator_status_word() gives the word's device address (int32),
+ * for reading it without synchronising.
+ */
+MOE_API int moe_operator_status(int32_t clear, int32_t* status, void* stream);
+MOE_API int moe_operator_status_word(int32_t** word);
 
 /* Library version: major * 10000 + minor * 100 + patch. */
 MOE_API int32_t moe_version(void);

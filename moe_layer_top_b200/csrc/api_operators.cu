@@ -72,6 +72,10 @@ int check_out_dtype(const char* what, int32_t dtype) {
 
 int run_product(moe::GroupedProblem& p, const char* what, void* stream) {
   MOE_TRY(moe::api_device_check(&p.num_sms));
+  if (!p.status) {
+    const cudaError_t e = moe::operator_status_word(&p.status);
+    if (e != cudaSuccess) return cuda_result(e, what);
+  }
   return cuda_result(moe::launch_grouped(p, static_cast<cudaStream_t>(stream)), what);
 }
 

@@ -28,7 +28,7 @@ struct GroupedProblem {
   long long ldo;           // fwd, dx: elements between the rows of out
   bool out_f32;            // else bf16
   bool accumulate;         // dw with out_f32: add to out
-  int* status;             // device status word, or NULL
+  int* status;             // device status word
   int num_sms;
 };
 

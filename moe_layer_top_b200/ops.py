@@ -50,7 +50,7 @@ EXPORTED = (
     "moe_combine_reduce_scatter", "moe_combine_reduce_scatter_emulated", "moe_rms_norm",
     "moe_rms_norm_backward_workspace_size", "moe_rms_norm_backward", "moe_quantize_rows_fp8",
     "moe_dequantize_rows_fp8", "moe_grouped_matmul", "moe_grouped_matmul_fp8", "moe_grouped_matmul_dx",
-    "moe_grouped_matmul_dw", "moe_matmul_fp8",
+    "moe_grouped_matmul_dw", "moe_matmul_fp8", "moe_operator_status", "moe_operator_status_word",
 )
 
 MAX_RANKS = 16
@@ -144,6 +144,8 @@ def lib():
             "moe_grouped_matmul_dw": (ctypes.c_int, [vp, i64, vp, i64, vp, i32, i32, i32, i32, vp, i32, i32, vp,
                                                      vp]),
             "moe_matmul_fp8": (ctypes.c_int, [vp, vp, vp, vp, i32, i32, i32, vp, i64, i32, vp, vp]),
+            "moe_operator_status": (ctypes.c_int, [i32, ctypes.POINTER(i32), vp]),
+            "moe_operator_status_word": (ctypes.c_int, [ctypes.POINTER(vp)]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -414,7 +416,8 @@ def combine_reduce_scatter_emulated(T, topk, H, ranks, epoch, timeout_us=2_000_0
 # ----------------------------------------------------------------------------- stand-alone operators
 # Tensors of other types, shapes, devices or layouts than a function documents raise ValueError here; what
 # the C ABI checks (sizes, alignment) raises MoeError.  The work runs on `stream`, or on the current stream
-# of the tensors' device; outputs and workspaces are allocated for that stream.
+# of the tensors' device; outputs and workspaces are allocated for that stream.  A wait inside a product's kernel that
+# runs out is recorded in `status` (int32 [1]) or, without it, in the device's word that operator_status() reads.
 _OUT_DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_FP32}
 
 
@@ -504,6 +507,16 @@ def _out(out, out_dtype, rows, cols, like):
 
 def _status(status, dev):
     return None if status is None else _flat("status", status, torch.int32, (1,), dev)
+
+
+def operator_status(device=None, clear=True, stream=None) -> int:
+    """The status of the products that were given no ``status`` on a device (default: the current one) and enqueued on
+    ``stream`` (default: its current stream) so far: MOE_STATUS_OK, or the first failure since it was last cleared.
+    Waits for the stream."""
+    st = ctypes.c_int32(-1)
+    with torch.cuda.device(device):
+        _check(lib().moe_operator_status(1 if clear else 0, ctypes.byref(st), _stream(stream)))
+    return int(st.value)
 
 
 def _offsets(offsets, G, dev):
