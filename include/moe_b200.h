@@ -495,7 +495,10 @@ MOE_API int moe_rms_norm_backward(const void* dy, int64_t lddy, const void* s, i
 MOE_API int moe_quantize_rows_fp8(const void* x, int64_t ldx, int64_t rows, int32_t cols, uint8_t* codes,
                                   float* scales, void* stream);
 
-/* FP8 rows -> bf16 rows x [rows, cols] (exact for scales that moe_quantize_rows_fp8 or moe_rms_norm wrote). */
+/*
+ * FP8 rows -> bf16 rows x [rows, cols]: exact for scales that moe_quantize_rows_fp8 or moe_rms_norm wrote, but that
+ * what exceeds bf16's largest finite number (rows with numbers from 248 * 2^120 on) becomes that number.
+ */
 MOE_API int moe_dequantize_rows_fp8(const uint8_t* codes, const float* scales, int64_t rows, int32_t cols, void* x,
                                     int64_t ldx, void* stream);
 

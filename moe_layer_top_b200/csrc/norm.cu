@@ -37,6 +37,15 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   return *reinterpret_cast<const uint4*>(&b);
 }
 
+// infinities -> the largest finite number of their sign
+__device__ __forceinline__ uint4 finite8(const uint4& u) {
+  bf16x8 b = *reinterpret_cast<const bf16x8*>(&u);
+  const __nv_bfloat162 most = __bfloat162bfloat162(__ushort_as_bfloat16(0x7f7f));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) b.h[i] = __hmax2_nan(__hmin2_nan(b.h[i], most), __hneg2(most));
+  return *reinterpret_cast<const uint4*>(&b);
+}
+
 // Two fp32 lanes in one register pair: half the instructions of these kernels, which issue at 70 % of the peak rate
 // (each lane is rounded as the scalar operation would be).
 using f2 = unsigned long long;
@@ -503,8 +512,10 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const __nv_bfloat16*
   }
 }
 
-// 16 codes per thread; the scale is a power of two, so bf16 holds the value exactly (subnormals of
-// bf16 aside, which the scale's floor of 2^-42 keeps out of reach)
+// 16 codes per thread; the scale is a power of two, so bf16 holds the value exactly (subnormals of bf16 aside, which
+// the scale's floor of 2^-42 keeps out of reach), but for one: from 248 * 2^120 on a row's largest number is rounded up
+// to the code of 256 at a scale of 2^120, and 2^128 is past bf16.  What is past bf16's largest finite number is read
+// back as that number, so that a finite row stays finite; NaN stays NaN.
 __global__ void __launch_bounds__(256) dequantize_rows_kernel(const uint8_t* codes, const float* scales,
                                                               long long rows, int cols, __nv_bfloat16* x,
                                                               long long ldx) {
@@ -534,7 +545,7 @@ __global__ void __launch_bounds__(256) dequantize_rows_kernel(const uint8_t* cod
       f[4 * j + 2] = v.z * s;
       f[4 * j + 3] = v.w * s;
     }
-    out[h] = pack8(f);
+    out[h] = finite8(pack8(f));
   }
   uint4* dst = reinterpret_cast<uint4*>(x + row * ldx + col);
   dst[0] = out[0];

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from moe_layer_top_b200 import ops
-from tests.operator_helpers import assert_within, product_bound
+from tests.operator_helpers import assert_within, product_bound, row_values
 
 pytestmark = pytest.mark.gpu
 
@@ -41,3 +41,26 @@ def test_a_reduction_that_takes_longer_than_the_limit_of_a_wait():
     assert int(status) == 0
     assert_within(dw[g], a.t() @ b, product_bound(a.t() @ b, a.abs().t() @ b.abs(), len(rows), torch.float32))
     assert not dw[:g].any() and not dw[g + 1:].any()
+
+
+@pytest.mark.parametrize("scale", [2.0 ** 120, 2.0 ** 127, 3.0e38])
+def test_codes_past_bf16_are_read_back_finite(scale):
+    """Every code at the largest scales: the bf16 value, or bf16's largest finite number; NaN codes stay NaN."""
+    codes = torch.arange(256, dtype=torch.uint8, device="cuda").view(2, 128)
+    scales = torch.full((1, 2), scale, device="cuda")
+    want = row_values(codes, scales)
+    most = torch.finfo(torch.bfloat16).max
+    back = ops.dequantize_rows_fp8(codes, scales).double()
+    nan = torch.isnan(want)
+    assert int(nan.sum()) == 2 and torch.equal(torch.isnan(back), nan)
+    assert torch.equal(back[~nan], want[~nan].clamp(-most, most).to(torch.bfloat16).double())
+
+
+def test_the_largest_rows_read_back_finite():
+    """x / 2^120 = 248 .. 255 rounds to the code of 256, which is 2^128."""
+    x = torch.zeros((3, 256), dtype=torch.bfloat16, device="cuda")
+    most = torch.finfo(torch.bfloat16).max
+    x[0, 3], x[1, 200], x[2, 7] = most, -248 * 2.0 ** 120, 247 * 2.0 ** 120
+    back = ops.dequantize_rows_fp8(*ops.quantize_rows_fp8(x))
+    assert back[0, 3] == most and back[1, 200] == -most and back[2, 7] == 240 * 2.0 ** 120
+    assert torch.isfinite(back).all()
