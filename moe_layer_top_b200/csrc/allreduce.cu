@@ -116,7 +116,10 @@ __device__ __forceinline__ bool reached(int v, uint32_t epoch) {
 }
 
 // one thread: bounded wait until *flag has reached this call's epoch; false
-// at once when the rank already gave up in this call (abort word = epoch)
+// at once when the rank already gave up in this call (abort word = epoch).
+// The status names the wait for a peer (kWhereArReady) wherever one was not
+// met: a wait for the rank's own chunks only follows from it, although it may
+// begin, and run out, earlier.
 __device__ bool wait_epoch(const int* flag, uint32_t epoch, int* abort_word, int* status,
                            unsigned long long timeout_ns, int where) {
   volatile int* ab = abort_word;
@@ -124,10 +127,12 @@ __device__ bool wait_epoch(const int* flag, uint32_t epoch, int* abort_word, int
   const uint64_t t0 = globaltimer_ns();
   while (true) {
     if (reached(ld_acquire_sys(flag), epoch)) return true;
-    if (reached(*ab, epoch)) return false;
-    if (globaltimer_ns() - t0 > timeout_ns) {
-      report_status(status, MOE_STATUS_WAIT_TIMEOUT | where);
-      *ab = static_cast<int>(epoch);
+    const bool gave_up = reached(*ab, epoch);
+    if (gave_up || globaltimer_ns() - t0 > timeout_ns) {
+      if (!gave_up || where == kWhereArReady) report_status(status, MOE_STATUS_WAIT_TIMEOUT | where);
+      if (where == kWhereArReady && status != nullptr)
+        atomicCAS(status, MOE_STATUS_WAIT_TIMEOUT | kWhereArDone, MOE_STATUS_WAIT_TIMEOUT | kWhereArReady);
+      if (!gave_up) *ab = static_cast<int>(epoch);
       return false;
     }
     __nanosleep(64);
@@ -216,8 +221,7 @@ __global__ void __launch_bounds__(kThreadsAr) combine_allreduce_kernel(const ArP
   }
 
   // 3. return once every chunk has been reduced: this rank's out is complete and no owner still
-  //    reads its partial (an owner may itself wait up to the limit in phase 2: a little longer
-  //    here, so that the status names that wait and not this one behind it)
+  //    reads its partial (an owner may itself wait up to the limit in phase 2: a little longer here)
   if (threadIdx.x == 0) {
     const unsigned long long limit = P.timeout_ns + P.timeout_ns / 8;
     for (int c = cta; c < P.nchunks; c += P.ctas_per_rank)
