@@ -574,6 +574,8 @@ cudaError_t launch_rms_norm(const RmsNormArgs& a, cudaStream_t stream) {
 namespace {
 
 constexpr int kWideSmem = 200 * 1024;
+static_assert(4 * 3 * 2 * 544 * 16 > kWideSmem && 2 * 3 * 2 * 1024 * 16 <= kWideSmem && 3 * 2 * 2 * 1024 * 16 <= kWideSmem,
+              "stages of the wide backward kernel");
 
 // the backward kernel's block: threads per row, rows at a time, vectors per thread
 struct BackwardShape {
@@ -608,9 +610,10 @@ cudaError_t launch_backward_rows(const RmsNormBackwardArgs& a, int blocks, cudaS
   const BackwardShape b = backward_shape(a.H);
   const size_t stage = static_cast<size_t>(kRes ? 3 : 2) * b.v * b.tx * 16;
   if (b.ty == 1 && b.v == 2) {  // two vectors per thread leave no registers to load ahead (16384 x 16384: 437 us, this way 380)
-    if (4 * stage <= kWideSmem) return launch_wide<2, 4, kRes>(a, blocks, b.tx, 4 * stage, stream);
-    if (3 * stage <= kWideSmem) return launch_wide<2, 3, kRes>(a, blocks, b.tx, 3 * stage, stream);
-    return launch_wide<2, 2, kRes>(a, blocks, b.tx, 2 * stage, stream);
+    // as many stages as fit: from 544 threads on three of three tensors or four of two, at 1024 two and three
+    constexpr int kMost = kRes ? 3 : 4;
+    if (kMost * stage <= kWideSmem) return launch_wide<2, kMost, kRes>(a, blocks, b.tx, kMost * stage, stream);
+    return launch_wide<2, kMost - 1, kRes>(a, blocks, b.tx, (kMost - 1) * stage, stream);
   }
   // With one vector two rows ahead are better than one where a block has many rows, unless there are three tensors
   // to read (T = 16384, H = 7168: 117 us instead of 132, with a residual gradient 174 instead of 155; T = 1024: 13.8
