@@ -149,10 +149,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* drain = acc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile uint32_t* beat = tmem_slot + 2;  // stages that the producer has filled
   int* scan = reinterpret_cast<int*>(reserve + 640);
   int* off = reinterpret_cast<int*>(reserve + 1024);
   int* first = off + kMaxGroups + 4;
-  static_assert((4 * C::kStages + 5) * 8 + 8 <= 640, "barriers overlap the scan buffer");
+  static_assert((4 * C::kStages + 5) * 8 + 12 <= 640, "barriers overlap the scan buffer");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cta = kPair || kSplit ? static_cast<int>(cluster_rank()) : 0;  // rank in the cluster
@@ -172,6 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
+    *beat = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tm_a);
     tma_prefetch_desc(&tm_b.map[0]);
@@ -216,6 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = warp_wait_bar(&empty[stage], phase ^ 1u, abort_flag, args.status, kWhereGroupedProducer);
         if (!ok) break;
         if (elect_lane()) {
+          *beat = static_cast<uint32_t>(fills) + 1;
           uint8_t* a = smem + static_cast<size_t>(stage) * C::kStageBytes;
           uint8_t* b = a + C::kABytes;
           uint32_t bar = smem_u32(&full[stage]);
@@ -341,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Tile tl = tile_at<Kind, Mode>(args, off, first, t);
         next_stage(tl.red / 64);
         if (tl.red % 64 == 0) continue;
-        ok = warp_wait_bar(&tail_full[stage], tails >> stage & 1u, abort_flag, args.status, kWhereGroupedMma, &empty[0]);
+        ok = warp_wait_bar(&tail_full[stage], tails >> stage & 1u, abort_flag, args.status, kWhereGroupedMma, beat);
         if (!ok) break;
         tails ^= 1u << stage;
         clear_tail(smem + static_cast<size_t>(stage) * C::kStageBytes, tl.red % 64);
@@ -374,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool any = red_begin(tl) < red_end(tl);  // otherwise there is no accumulator: zeros
       if (any) {
         // (over a tile's whole reduction: up to 2^30 long, seconds)
-        if (!warp_wait_bar(&acc_full[abuf], aphase, abort_flag, args.status, kWhereGroupedEpilogue, &empty[0])) break;
+        if (!warp_wait_bar(&acc_full[abuf], aphase, abort_flag, args.status, kWhereGroupedEpilogue, beat)) break;
         tc_fence_after();
       }
       if constexpr (Kind != kGroupedDw) {

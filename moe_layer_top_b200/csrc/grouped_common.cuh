@@ -25,35 +25,23 @@ constexpr int kPartialPitch = 132;
 constexpr int kWhereGroupedProducer = 0x41, kWhereGroupedMma = 0x42, kWhereGroupedEpilogue = 0x43,
               kWhereGroupedDrain = 0x44;
 
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.relaxed.cta.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
 // Bounded wait: polls the barrier, looking at the abort flag and the clock every 256 polls only.  `beat`, for a wait
-// that spans a whole reduction: a barrier that flips as long as the reduction goes on (one of the ring's stages, every
-// microsecond or two); the limit then holds for the time since it was last seen to have flipped.
+// that spans a whole reduction: the number of stages that this CTA's producer has filled, which goes on counting as
+// long as the reduction goes on; the limit then holds for the time since it was last seen to have changed.
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort, int* status, int where,
-                                         uint64_t* beat = nullptr) {
+                                         const volatile uint32_t* beat = nullptr) {
   uint64_t t0 = 0;
-  bool seen = false;
+  uint32_t seen = 0;
   for (uint32_t i = 1;; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
     if ((i & 255) == 0) {
       if (*abort) return false;
       const uint64_t now = globaltimer_ns();
-      if (beat != nullptr && mbar_test(beat, 0) != seen) {
-        seen = !seen;
+      if (t0 == 0) t0 = now;
+      if (beat != nullptr && *beat != seen) {
+        seen = *beat;
         t0 = now;
       }
-      if (t0 == 0) t0 = now;
       if (now - t0 > kWaitTimeoutNs) {
         *abort = 1;
         report_status(status, MOE_STATUS_WAIT_TIMEOUT | where);
@@ -64,7 +52,7 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatil
 }
 
 __device__ __forceinline__ bool warp_wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort, int* status,
-                                              int where, uint64_t* beat = nullptr) {
+                                              int where, const volatile uint32_t* beat = nullptr) {
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;  // the common case, without the bookkeeping
   const bool ok = wait_bar(bar, parity, abort, status, where, beat);
   return __all_sync(0xffffffffu, ok);
