@@ -34,10 +34,15 @@
 // double-buffered in TMEM, so a tile's stores run under the next tile's
 // products.
 //
-// On a B200: 8192 x 4096 x 4096 forward and dx 177 us (1550 TFLOP/s, 0.94 of
-// the measured peak), dw 197 us; 32768 rows over 128 experts of 4096 x 1536
-// forward and dx 405 us, dw 510 us (bound by the power limit with HBM and the
-// tensor cores both busy); 512 rows over the same experts 244 us, 0.99 of HBM.
+// On a B200: 8192 x 4096 x 4096 forward and dx 176 us (1560 TFLOP/s, 0.95 of
+// the measured peak), dw 191 us; 32768 rows over 128 experts of 4096 x 1536
+// forward and dx 400 us, dw 500 us; 512 rows over the same experts 243 us,
+// 0.99 of HBM.  Forward and dx of that training batch are bound by the power
+// limit (dx: a launch by itself 377 us at 1965 MHz, back to back 477 us at
+// 1005 MHz).  dw is not: by itself it takes 519 us at 1965 MHz, the tensor
+// pipe 39 % active and DRAM at half its rate.  Its reductions are four stages
+// long, and it waits between them: stores and products hardly overlap (278 us
+// without its stores, 273 without its products).
 #include "grouped_common.cuh"
 
 namespace moe {

@@ -15,7 +15,8 @@
 // registers between the sum and the output, 16 bytes per access.  On a B200
 // (6551 GB/s of copy): 8192 x 7168 with residual and FP8 output 63 us, 0.99 of
 // the copy rate; backward of 16384 x 4096 with a residual gradient 86 us, 0.96;
-// quantising 8192 x 7168 34 us, 0.79; reading it back 29 us, 0.94.
+// quantising 8192 x 7168 34 us, 0.79; reading it back 29 us, 0.94.  The
+// backward pass of narrow rows is further off: 32768 x 512 24 us, 0.63.
 #include "common.cuh"
 #include "kernels.h"
 #include "rows.h"
